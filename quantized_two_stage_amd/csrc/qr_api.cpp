@@ -69,6 +69,10 @@ namespace {
 
 thread_local char g_err[512] = "";
 
+}  // namespace
+
+namespace qr {
+
 int fail(int code, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -87,6 +91,13 @@ int hip_status(hipError_t e, const char* what) {
     return fail(QR_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
   return ok();
 }
+
+}  // namespace qr
+
+namespace {
+
+using qr::fail;
+using qr::hip_status;
 
 bool w_sim(int W) { return W == 2 || W == 4 || W == 8; }
 

@@ -32,6 +32,14 @@ struct Layout {
 };
 
 bool codec_valid(int codec);
+
+// The text of the last error on this thread (qr_last_error): fail() sets it
+// and returns `code`, ok() clears it and returns QR_OK, hip_status() does the
+// one or the other for the outcome of a HIP call.
+int fail(int code, const char* fmt, ...);
+int ok();
+int hip_status(hipError_t e, const char* what);
+
 Layout make_layout(int codec, size_t n);
 
 struct InPtrs { const uint8_t* p[kMaxRanks]; };

@@ -1,0 +1,471 @@
+// qr_rows.hip -- gfx950 kernels of the row operators of include/qr_layer.h:
+// root-mean-square norm with the residual's addition (from 16-bit rows or
+// from a wire image) and the gated activation, both to 8-bit codes with one
+// scale a row.
+//
+// One pass over HBM.  A workgroup (or, for short rows, a wave) holds a whole
+// row in registers: it loads its vectors of 8 values, writes h, keeps the
+// values u that are to be coded, reduces the sum of squares and the largest
+// magnitude across the row once, and codes from the registers.  That a single
+// reduction is enough rests on the norm's factor r being common to the row:
+// u_i*r*127/(a*r) = u_i*127/a, so the codes need the maximum a of u = h*weight
+// alone, and r enters the scale only.
+#include "qr.h"
+#include "qr_device.h"
+#include "qr_layer_internal.h"
+
+namespace qr {
+namespace {
+
+// A vector is 8 values, 16 bytes, at any 2-byte address (rows of odd length
+// or stride): gfx950 runs with unaligned access enabled, and a memcpy of
+// known size becomes one global_load_dwordx4 whatever the alignment.
+__device__ __forceinline__ u32x4 load8(const uint8_t* p) {
+  u32x4 v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+__device__ __forceinline__ void store8(uint8_t* p, u32x4 v) { __builtin_memcpy(p, &v, 16); }
+
+// The first n values of the vector at p, zeros after them.  Rows of 8 values or
+// more: a row's last, short vector is read as the 16 bytes that end where the
+// row ends and shifted down, one load whatever n is.
+__device__ __forceinline__ u32x4 load_n(const uint8_t* p, uint32_t n) {
+  const uint32_t miss = 8 - n;
+  u32x4 v = load8(p - 2 * miss);
+  if (miss != 0) {
+    uint64_t lo = v.x | (uint64_t)v.y << 32, hi = v.z | (uint64_t)v.w << 32;
+    if (miss >= 4) {
+      lo = hi;
+      hi = 0;
+    }
+    const uint32_t sh = 16 * (miss & 3);
+    lo = lo >> sh | (hi << 1) << (63 - sh);
+    hi >>= sh;
+    v = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+  }
+  return v;
+}
+// the same, value by value, for rows of any length
+__device__ __forceinline__ u32x4 load_each(const uint8_t* p, uint32_t n) {
+  if (n == 8) return load8(p);
+  uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+  for (uint32_t i = 0; i < n; i++) {
+    const uint64_t v = reinterpret_cast<const uint16_t*>(p)[i];
+    if (i < 4) lo |= v << (16 * i);
+    else hi |= v << (16 * (i - 4));
+  }
+  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+template <bool Each>
+__device__ __forceinline__ u32x4 load_vec(const uint8_t* p, uint32_t n) {
+  return Each ? load_each(p, n) : load_n(p, n);
+}
+__device__ __forceinline__ void store_n(uint8_t* p, u32x4 v, uint32_t n) {
+  if (n == 8) {
+    store8(p, v);
+    return;
+  }
+  const uint64_t lo = v.x | (uint64_t)v.y << 32, hi = v.z | (uint64_t)v.w << 32;
+#pragma unroll 1
+  for (uint32_t i = 0; i < n; i++)
+    reinterpret_cast<uint16_t*>(p)[i] =
+        (uint16_t)(i < 4 ? lo >> (16 * i) : hi >> (16 * (i - 4)));
+}
+
+template <int D>
+__device__ __forceinline__ void widen(u32x4 v, float (&f)[8]) {
+#pragma unroll
+  for (int k = 0; k < 4; k++) {
+    f[2 * k] = ld16<D>(v[k] & 0xffffu);
+    f[2 * k + 1] = ld16<D>(v[k] >> 16);
+  }
+}
+
+// max(a, |v|) that keeps a NaN (v_maximum3_f32)
+__device__ __forceinline__ float max_abs(float a, float v) {
+  return __builtin_elementwise_maximum(a, __builtin_fabsf(v));
+}
+
+// Words of quarter j (0..3) of a block's codes in a planar wire image: 8 codes
+// = 8*b bits starting at bit 8*b*j of the block's bitstring, the first code at
+// bit 0 (6-bit quarters 1 and 3 start in the middle of a word).
+template <int C>
+__device__ __forceinline__ void quarter_words(const uint8_t* blk, int j, u32x4& w) {
+  constexpr int b = CodecT<C>::bits;
+  if constexpr (b == 4) {
+    w[0] = reinterpret_cast<const uint32_t*>(blk)[j];
+  } else if constexpr (b == 8) {
+    const u32x2 q = reinterpret_cast<const u32x2*>(blk)[j];
+    w[0] = q.x;
+    w[1] = q.y;
+  } else {                                           // bits [48j, 48j+48)
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(blk) + ((3 * j) >> 1);
+    const uint32_t lo = p[0], hi = p[1];
+    const int sh = (j & 1) * 16;
+    w[0] = __builtin_amdgcn_alignbit(hi, lo, sh);
+    w[1] = hi >> sh;
+  }
+}
+
+// type of the 16-bit buffers under the wire's type: with the cast option the
+// wire holds binary16 and the buffers bfloat16
+template <int D>
+constexpr int kBufType = D == kBF16H ? (int)kBF16 : D;
+
+// ---------------------------------------------------------------------------
+// operators: what a row's vector is read from, and the values to be coded
+
+// C < 0: x from 16-bit rows; else from the planar wire image of codec C.
+template <int D, int C>
+struct Norm {
+  static constexpr bool kNorm = true;
+  static constexpr int B = kBufType<D>;
+  NormArgs a;
+
+  struct Raw {
+    u32x4 x;               // 16-bit values; for a wire its code words (x, y)
+    uint32_t s, z;         // the wire block's scale and zero
+    u32x4 res, w;
+  };
+  struct Row {
+    const uint8_t *x, *res;
+    uint8_t* h;
+    uint32_t vec0;         // the row's first vector in the wire image
+  };
+
+  __device__ __forceinline__ Row row(uint32_t m, uint32_t d) const {
+    Row r;
+    r.x = C < 0 ? a.x + 2 * (size_t)m * a.ldx : a.x;
+    r.res = a.residual ? a.residual + 2 * (size_t)m * a.ldr : nullptr;
+    r.h = a.h ? a.h + 2 * (size_t)m * a.ldh : nullptr;
+    r.vec0 = C < 0 ? 0u : m * (d / 8);
+    return r;
+  }
+  template <bool Each>
+  __device__ __forceinline__ void load(const Row& r, uint32_t vec, uint32_t n, Raw& v) const {
+    if constexpr (C < 0) {
+      v.x = load_vec<Each>(r.x + 16 * (size_t)vec, n);
+    } else if constexpr (C == kFP) {
+      v.x = load8(r.x + 16 * (size_t)(r.vec0 + vec));
+    } else {
+      const uint32_t q = r.vec0 + vec;
+      quarter_words<C>(r.x + (size_t)(q >> 2) * CodecT<C>::block_bytes, q & 3, v.x);
+      v.s = reinterpret_cast<const uint16_t*>(r.x + a.off_s)[q >> 2];
+      if constexpr (CodecT<C>::asym)
+        v.z = reinterpret_cast<const uint16_t*>(r.x + a.off_z)[q >> 2];
+    }
+    if (r.res) v.res = load_vec<Each>(r.res + 16 * (size_t)vec, n);
+    v.w = load_vec<Each>(a.weight + 16 * (size_t)vec, n);
+  }
+  // u and the sum of squares, and h written
+  __device__ __forceinline__ void values(const Row& r, uint32_t vec, uint32_t n, const Raw& v,
+                                         float (&u)[8], float& ss) const {
+    u32x4 h;
+    if constexpr (C < 0) {
+      h = v.x;
+    } else if constexpr (C == kFP) {
+      h = v.x;
+      if constexpr (D == kBF16H)
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+          h[k] = st16x2<kBF16>(h2f(v.x[k] & 0xffffu), h2f(v.x[k] >> 16));
+    } else {
+      using T = CodecT<C>;
+      uint32_t w[2] = {v.x[0], T::bits > 4 ? v.x[1] : 0u};
+      float cv[8];
+      code_values<C, 8>(w, cv);
+      const float s = h2f(v.s) * T::unpack_scale;
+      const float z = T::asym ? h2f(v.z) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; i++) cv[i] = T::asym ? __builtin_fmaf(cv[i], s, z) : cv[i] * s;
+#pragma unroll
+      for (int k = 0; k < 4; k++) h[k] = st16x2<D>(cv[2 * k], cv[2 * k + 1]);
+    }
+    float hv[8];
+    widen<B>(h, hv);
+    if (r.res) {
+      float rv[8];
+      widen<B>(v.res, rv);
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+        h[k] = st16x2<B>(hv[2 * k] + rv[2 * k], hv[2 * k + 1] + rv[2 * k + 1]);
+      widen<B>(h, hv);
+    }
+    if (r.h) store_n(r.h + 16 * (size_t)vec, h, n);
+    weigh(hv, v.w, u, ss);
+  }
+  __device__ __forceinline__ void weigh(const float (&hv)[8], u32x4 w, float (&u)[8],
+                                        float& ss) const {
+    float wv[8];
+    widen<B>(w, wv);
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      ss = __builtin_fmaf(hv[i], hv[i], ss);
+      u[i] = hv[i] * wv[i];
+    }
+  }
+  // u of a vector whose h this lane has written (or x, where h is not)
+  template <bool Each>
+  __device__ __forceinline__ void again(const Row& r, uint32_t vec, uint32_t n,
+                                        float (&u)[8]) const {
+    const uint8_t* p = (r.h ? r.h : r.x) + 16 * (size_t)vec;
+    float hv[8], unused = 0.0f;
+    widen<B>(load_vec<Each>(p, n), hv);
+    weigh(hv, load_vec<Each>(a.weight + 16 * (size_t)vec, n), u, unused);
+  }
+  __device__ __forceinline__ float factor(float ss, uint32_t d) const {
+    return 1.0f / __builtin_sqrtf(ss / (float)d + a.eps);
+  }
+};
+
+template <int D>
+struct Silu {
+  static constexpr bool kNorm = false;
+  const uint8_t* gu;
+  size_t ldg;
+
+  struct Raw {
+    u32x4 g, u;
+  };
+  struct Row {
+    const uint8_t *g, *u;
+  };
+  __device__ __forceinline__ Row row(uint32_t m, uint32_t d) const {
+    const uint8_t* p = gu + 2 * (size_t)m * ldg;
+    return Row{p, p + 2 * (size_t)d};
+  }
+  template <bool Each>
+  __device__ __forceinline__ void load(const Row& r, uint32_t vec, uint32_t n, Raw& v) const {
+    v.g = load_vec<Each>(r.g + 16 * (size_t)vec, n);
+    v.u = load_vec<Each>(r.u + 16 * (size_t)vec, n);
+  }
+  // g / (1 + exp(-g)) * u.  exp by v_exp_f32 (2^x): the rounding of the
+  // exponent costs |g| * 2^-24 relative to exp(-g), which matters only where
+  // exp(-g) is large, that is where the value is near zero; v_rcp_f32 is
+  // within one unit in the last place.  exp(-g) = inf gives g * 0.
+  __device__ __forceinline__ void values(const Row&, uint32_t, uint32_t, const Raw& v,
+                                         float (&u)[8], float&) const {
+    float g[8];
+    widen<D>(v.g, g);
+    widen<D>(v.u, u);
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const float e = __builtin_amdgcn_exp2f(g[i] * -1.44269504088896341f);
+      u[i] = g[i] * __builtin_amdgcn_rcpf(1.0f + e) * u[i];
+    }
+  }
+  template <bool Each>
+  __device__ __forceinline__ void again(const Row& r, uint32_t vec, uint32_t n,
+                                        float (&u)[8]) const {
+    Raw v;
+    float unused;
+    load<Each>(r, vec, n, v);
+    values(r, vec, n, v, u, unused);
+  }
+  __device__ __forceinline__ float factor(float, uint32_t) const { return 1.0f; }
+};
+
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) v = __builtin_elementwise_maximum(v, __shfl_xor(v, m));
+  return v;
+}
+
+// over the T lanes of a row; T > 64: through LDS, every lane gets the result
+template <int T, bool Sum>
+__device__ __forceinline__ void row_reduce(float& ss, float& a, float* lds) {
+  if (Sum) ss = wave_sum(ss);
+  a = wave_max(a);
+  if constexpr (T > 64) {
+    constexpr int nw = T / 64;
+    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    if (lane == 0) {
+      if (Sum) lds[wave] = ss;
+      lds[nw + wave] = a;
+    }
+    __syncthreads();
+    ss = 0.0f;
+    a = 0.0f;
+#pragma unroll
+    for (int w = 0; w < nw; w++) {
+      if (Sum) ss += lds[w];
+      a = __builtin_elementwise_maximum(a, lds[nw + w]);
+    }
+  }
+}
+
+// 8 codes; f = 0 marks a row without codes
+__device__ __forceinline__ u32x2 code8(const float (&u)[8], float f) {
+  u32x2 w = {0u, 0u};
+  if (f != 0.0f) {
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+      uint32_t b;
+      rint_byte<0>(b, u[4 * k] * f);
+      rint_byte<1>(b, u[4 * k + 1] * f);
+      rint_byte<2>(b, u[4 * k + 2] * f);
+      rint_byte<3>(b, u[4 * k + 3] * f);
+      w[k] = b;
+    }
+  }
+  return w;
+}
+__device__ __forceinline__ void store_codes(int8_t* p, u32x2 w, uint32_t n) {
+  if (n == 8) {
+    __builtin_memcpy(p, &w, 8);
+  } else {
+    const uint64_t v = w.x | (uint64_t)w.y << 32;
+#pragma unroll 1
+    for (uint32_t i = 0; i < n; i++) p[i] = (int8_t)(v >> (8 * i));
+  }
+}
+
+// f = 127 / a (0: the row has no codes) and the row's scale
+template <class Op>
+__device__ __forceinline__ float row_scale(const Op& op, float ss, float a, uint32_t d,
+                                           float& scale) {
+  constexpr float kTiny = 0x1p-119f, kInf = __builtin_inff();
+  const float r = op.factor(ss, d);
+  const bool fine = a < kInf && (!Op::kNorm || ss < kInf);    // false for NaN
+  const bool use = fine && a >= kTiny;
+  scale = use ? a * r / 127.0f : fine ? 0.0f : __builtin_nanf("");
+  return use ? 127.0f / a : 0.0f;
+}
+
+constexpr int rows_per_group(int T) { return T == 64 ? 4 : 1; }
+
+// T lanes to a row of at most 8*T*V values, held in registers
+template <class Op, int T, int V>
+__global__ __launch_bounds__(T * rows_per_group(T)) void k_rows(Op op, RowsOut o) {
+  constexpr int R = rows_per_group(T);
+  __shared__ float lds[2 * (T / 64)];
+  const uint32_t t = threadIdx.x % T;
+  for (uint32_t m = blockIdx.x * R + threadIdx.x / T; m < o.M; m += gridDim.x * R) {
+    const auto row = op.row(m, o.d);
+    typename Op::Raw raw[V];
+    float u[V][8];
+    float ss = 0.0f, a = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; j++) {
+      const uint32_t i0 = 8 * (t + T * j);
+      if (i0 < o.d) op.template load<false>(row, t + T * j, o.d - i0 < 8 ? o.d - i0 : 8, raw[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < V; j++) {
+      const uint32_t i0 = 8 * (t + T * j);
+      if (i0 < o.d) {
+        op.values(row, t + T * j, o.d - i0 < 8 ? o.d - i0 : 8, raw[j], u[j], ss);
+#pragma unroll
+        for (int i = 0; i < 8; i++) a = max_abs(a, u[j][i]);
+      }
+    }
+    row_reduce<T, Op::kNorm>(ss, a, lds);
+    float scale;
+    const float f = row_scale(op, ss, a, o.d, scale);
+    int8_t* q = o.q + (size_t)m * o.ldq;
+#pragma unroll
+    for (int j = 0; j < V; j++) {
+      const uint32_t i0 = 8 * (t + T * j);
+      if (i0 < o.d) store_codes(q + i0, code8(u[j], f), o.d - i0 < 8 ? o.d - i0 : 8);
+    }
+    if (t == 0) o.scales[m] = scale;
+    if (T > 64 && m + gridDim.x < o.M) __syncthreads();       // lds is used again
+  }
+}
+
+// rows of any length: a second pass reads the row again to code it (each lane
+// what it has itself written or read)
+template <class Op, int T>
+__global__ __launch_bounds__(T) void k_rows_long(Op op, RowsOut o) {
+  __shared__ float lds[2 * (T / 64)];
+  for (uint32_t m = blockIdx.x; m < o.M; m += gridDim.x) {
+    const auto row = op.row(m, o.d);
+    float ss = 0.0f, a = 0.0f;
+    for (uint32_t vec = threadIdx.x; 8 * vec < o.d; vec += T) {
+      const uint32_t n = o.d - 8 * vec < 8 ? o.d - 8 * vec : 8;
+      typename Op::Raw raw;
+      float u[8];
+      op.template load<true>(row, vec, n, raw);
+      op.values(row, vec, n, raw, u, ss);
+#pragma unroll
+      for (int i = 0; i < 8; i++) a = max_abs(a, u[i]);
+    }
+    row_reduce<T, Op::kNorm>(ss, a, lds);
+    float scale;
+    const float f = row_scale(op, ss, a, o.d, scale);
+    int8_t* q = o.q + (size_t)m * o.ldq;
+    for (uint32_t vec = threadIdx.x; 8 * vec < o.d; vec += T) {
+      const uint32_t n = o.d - 8 * vec < 8 ? o.d - 8 * vec : 8;
+      float u[8];
+      op.template again<true>(row, vec, n, u);
+      store_codes(q + 8 * vec, code8(u, f), n);
+    }
+    if (threadIdx.x == 0) o.scales[m] = scale;
+    if (m + gridDim.x < o.M) __syncthreads();
+  }
+}
+
+template <class Op>
+hipError_t launch_rows(const Op& op, const RowsOut& o, hipStream_t st) {
+  constexpr uint32_t kMaxGroups = 1u << 21;       // times 1024 lanes: below 2^32
+  const auto groups = [&](uint32_t R) {
+    const uint32_t g = (o.M + R - 1) / R;
+    return dim3(g < kMaxGroups ? g : kMaxGroups);
+  };
+  if (o.d < 8)
+    k_rows_long<Op, 64><<<groups(1), 64, 0, st>>>(op, o);
+  else if (o.d <= 2048)
+    k_rows<Op, 64, 4><<<groups(4), 256, 0, st>>>(op, o);
+  else if (o.d <= 8192)
+    k_rows<Op, 256, 4><<<groups(1), 256, 0, st>>>(op, o);
+  else if (o.d <= 32768)
+    k_rows<Op, 1024, 4><<<groups(1), 1024, 0, st>>>(op, o);
+  else
+    k_rows_long<Op, 1024><<<groups(1), 1024, 0, st>>>(op, o);
+  return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_wire(int codec, const NormArgs& a, const RowsOut& o, hipStream_t st) {
+  switch (codec) {
+    case kFP: return launch_rows(Norm<D, kFP>{a}, o, st);
+    case kQ8: return launch_rows(Norm<D, kQ8>{a}, o, st);
+    case kQ6: return launch_rows(Norm<D, kQ6>{a}, o, st);
+    case kQ4: return launch_rows(Norm<D, kQ4>{a}, o, st);
+    case kFP8: return launch_rows(Norm<D, kFP8>{a}, o, st);
+    case kQ8A: return launch_rows(Norm<D, kQ8A>{a}, o, st);
+    case kQ6A: return launch_rows(Norm<D, kQ6A>{a}, o, st);
+    default: return launch_rows(Norm<D, kQ4A>{a}, o, st);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_norm(int codec, int dtype, const NormArgs& a, const RowsOut& o,
+                       hipStream_t st) {
+  if (codec < 0)
+    return dtype == kF16 ? launch_rows(Norm<kF16, -1>{a}, o, st)
+                         : launch_rows(Norm<kBF16, -1>{a}, o, st);
+  switch (dtype) {
+    case kF16: return launch_wire<kF16>(codec, a, o, st);
+    case kBF16: return launch_wire<kBF16>(codec, a, o, st);
+    default: return launch_wire<kBF16H>(codec, a, o, st);
+  }
+}
+
+hipError_t launch_silu(int dtype, const uint8_t* gu, size_t ldg, const RowsOut& o,
+                       hipStream_t st) {
+  return dtype == kF16 ? launch_rows(Silu<kF16>{gu, ldg}, o, st)
+                       : launch_rows(Silu<kBF16>{gu, ldg}, o, st);
+}
+
+}  // namespace qr

@@ -1,4 +1,5 @@
-"""Python binding of the C ABI in include/qr.h (argument marshalling only).
+"""Python binding of the C ABI in include/qr.h and include/qr_layer.h (argument
+marshalling only).
 
 Every function has the name of the C entry point it calls and takes torch
 tensors on the GPU; all work happens in libqr.so's HIP kernels, on the current
@@ -38,7 +39,7 @@ def _load():
         raise ImportError("libqr.so is not built (%s); run "
                           "quantized_two_stage_amd/build.py" % LIB_PATH)
     L = ctypes.CDLL(LIB_PATH)
-    sz, i32, P = ctypes.c_size_t, ctypes.c_int, ctypes.c_void_p
+    sz, i32, f32, P = ctypes.c_size_t, ctypes.c_int, ctypes.c_float, ctypes.c_void_p
     PP = ctypes.POINTER(ctypes.c_void_p)
     sig = {
         "qr_wire_bytes": (sz, [i32, sz]),
@@ -55,6 +56,12 @@ def _load():
         "qr_allreduce_oneshot": (i32, [i32, i32, PP, PP, sz, P]),
         "qr_allreduce_sim_noalloc": (i32, [i32, i32, i32, PP, PP, sz, P]),
         "qr_last_error": (ctypes.c_char_p, []),
+        "qr_add_rmsnorm_q8": (i32, [i32, P, sz, P, sz, P, f32, sz, sz, P, sz, P, sz, P, P]),
+        "qr_gather_add_rmsnorm_q8": (i32, [i32, i32, P, P, sz, P, f32, sz, sz, P, sz, P, sz, P,
+                                           P]),
+        "qr_silu_mul_q8": (i32, [i32, P, sz, sz, sz, P, sz, P, P]),
+        "qr_gemm_i8": (i32, [i32, P, sz, P, P, sz, P, P, sz, sz, sz, P, sz, P, sz, P]),
+        "qr_gemm_i8_workspace_bytes": (sz, [sz, sz, sz]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -67,7 +74,8 @@ EXPORTS = ("qr_wire_bytes", "qr_sim_workspace_bytes", "qr_recv_bytes", "qr_quant
            "qr_dequantize", "qr_quantize_ranks", "qr_quantize_recv", "qr_reduce_stage1",
            "qr_reduce_recv", "qr_gather_stage2",
            "qr_allreduce_sim", "qr_allreduce_oneshot", "qr_allreduce_sim_noalloc",
-           "qr_last_error")
+           "qr_last_error", "qr_add_rmsnorm_q8", "qr_gather_add_rmsnorm_q8", "qr_silu_mul_q8",
+           "qr_gemm_i8", "qr_gemm_i8_workspace_bytes")
 
 
 def _check(rc):
@@ -250,3 +258,183 @@ def alloc_recv(W, codec, n, device="cuda"):
 def alloc_workspace(W, codec, n, device="cuda"):
     return torch.empty(qr_sim_workspace_bytes(W, codec, n), dtype=torch.uint8,
                        device=device)
+
+
+# ---------------------------------------------------------------------------
+# the operators between two allreduces (include/qr_layer.h)
+
+_DTYPES = {torch.float16: QR_FP16, torch.bfloat16: QR_BF16}
+
+
+def _type16(t, what):
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError("%s is %s: float16 or bfloat16 expected" % (what, t.dtype))
+    return code
+
+
+def _mat(what, t, rows, cols, dtype, dev):
+    """A matrix argument: its row stride in elements (rows contiguous)."""
+    if t.dtype is not dtype:
+        raise TypeError("%s is %s: %s expected" % (what, t.dtype, dtype))
+    if t.shape != (rows, cols):
+        raise ValueError("%s has shape %s: %s expected" % (what, tuple(t.shape), (rows, cols)))
+    if t.get_device() != dev:
+        raise ValueError("%s is not on GPU %d" % (what, dev))
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError("%s: the values of a row are not contiguous" % what)
+    return ld if rows > 1 else max(ld, cols)
+
+
+def _vec(what, t, n, dtype, dev):
+    if t.dtype is not dtype:
+        raise TypeError("%s is %s: %s expected" % (what, t.dtype, dtype))
+    if t.numel() != n:
+        raise ValueError("%s holds %d values: %d expected" % (what, t.numel(), n))
+    if t.get_device() != dev:
+        raise ValueError("%s is not on GPU %d" % (what, dev))
+    if not t.is_contiguous():
+        raise ValueError("%s is not contiguous" % what)
+    return t.data_ptr()
+
+
+def _codes(what, t, rows, cols, dev):
+    """A matrix of codes that qr_gemm_i8 reads: rows of whole 16-byte pieces,
+    the last one's padding inside the tensor's storage."""
+    ld = _mat(what, t, rows, cols, torch.int8, dev)
+    if rows == 1:
+        ld = -(-ld // 16) * 16
+    if rows > 0 and (t.storage_offset() + (rows - 1) * ld + -(-cols // 16) * 16
+                     > t.untyped_storage().nbytes()):
+        raise ValueError("%s: the padding of its last row up to a multiple of 16 is outside "
+                         "its storage (alloc_q8 makes room for it)" % what)
+    return ld
+
+
+def _device(t, what):
+    """The current GPU, which the tensors of a call must be on."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("%s is not on the current GPU" % what)
+    return dev
+
+
+def _stream_on(dev, stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+def _matrix_shape(what, t):
+    if t.dim() != 2:
+        raise ValueError("%s has %d dimensions: a matrix expected" % (what, t.dim()))
+    return t.shape
+
+
+def _norm_args(residual, weight, h, q, scales, M, d, dtype, dev):
+    ldr = _mat("residual", residual, M, d, dtype, dev) if residual is not None else 0
+    ldh = _mat("h", h, M, d, dtype, dev) if h is not None else 0
+    return (residual.data_ptr() if residual is not None else None, ldr,
+            _vec("weight", weight, d, dtype, dev),
+            h.data_ptr() if h is not None else None, ldh,
+            q.data_ptr(), _mat("q", q, M, d, torch.int8, dev),
+            _vec("scales", scales, M, torch.float32, dev))
+
+
+def qr_add_rmsnorm_q8(x, residual, weight, eps, h, q, scales, stream=None):
+    """h = x + residual; q, scales = the 8-bit codes and row scales of h's
+    root-mean-square norm times weight.  residual and h may be one tensor
+    (updated in place), or both None (h = x).  Matrices are [M, d] with
+    contiguous rows, scales holds M float32."""
+    M, d = _matrix_shape("x", x)
+    code = _type16(x, "x")
+    dev = _device(x, "x")
+    ldx = _mat("x", x, M, d, x.dtype, dev)
+    pr, ldr, pw, ph, ldh, pq, ldq, ps = _norm_args(residual, weight, h, q, scales, M, d, x.dtype,
+                                                   dev)
+    _check(LIB.qr_add_rmsnorm_q8(code, x.data_ptr(), ldx, pr, ldr, pw, eps, M, d, ph, ldh, pq,
+                                 ldq, ps, _stream_on(dev, stream)))
+    return h, q, scales
+
+
+def qr_gather_add_rmsnorm_q8(codec, wire, residual, weight, eps, h, q, scales, dtype=None,
+                             stream=None):
+    """qr_add_rmsnorm_q8 of the values that a wire image of h.numel() elements
+    holds (residual may be None: h = the values).  dtype: QR_BF16_VIA_FP16 for
+    bfloat16 buffers under the cast option."""
+    M, d = _matrix_shape("h", h)
+    code = _type16(h, "h") if dtype is None else dtype
+    if h.dtype is not (torch.float16 if code == QR_FP16 else torch.bfloat16):
+        raise TypeError("h is %s under dtype %d" % (h.dtype, code))
+    dev = _device(h, "h")
+    if wire.get_device() != dev or not wire.is_contiguous():
+        raise ValueError("wire is not contiguous on GPU %d" % dev)
+    if M * d > 0 and _nbytes(wire) < qr_wire_bytes(codec, M * d):
+        raise ValueError("wire holds %d bytes, %d needed" % (_nbytes(wire),
+                                                             qr_wire_bytes(codec, M * d)))
+    pr, ldr, pw, ph, ldh, pq, ldq, ps = _norm_args(residual, weight, h, q, scales, M, d, h.dtype,
+                                                   dev)
+    _check(LIB.qr_gather_add_rmsnorm_q8(codec, code, wire.data_ptr(), pr, ldr, pw, eps, M, d, ph,
+                                        ldh, pq, ldq, ps, _stream_on(dev, stream)))
+    return h, q, scales
+
+
+def qr_silu_mul_q8(gu, q, scales, stream=None):
+    """q, scales = the 8-bit codes and row scales of silu(gate) * up, where a
+    row of gu ([M, 2d]) holds the d gate values and then the d up values."""
+    M, d2 = _matrix_shape("gu", gu)
+    if d2 % 2 != 0:
+        raise ValueError("gu has rows of %d values: gate and up differ in length" % d2)
+    d = d2 // 2
+    code = _type16(gu, "gu")
+    dev = _device(gu, "gu")
+    _check(LIB.qr_silu_mul_q8(code, gu.data_ptr(), _mat("gu", gu, M, d2, gu.dtype, dev), M, d,
+                              q.data_ptr(), _mat("q", q, M, d, torch.int8, dev),
+                              _vec("scales", scales, M, torch.float32, dev),
+                              _stream_on(dev, stream)))
+    return q, scales
+
+
+def qr_gemm_i8(a, sa, b, sb, c, bias=None, workspace=None, stream=None):
+    """c = (a @ b^T in 32-bit integers) * sa * sb (+ bias), rounded once to c's
+    type.  a: [M, K] int8 codes of the tokens and sa their M float32 scales,
+    b: [N, K] int8 codes of the weights and sb their N scales; workspace:
+    alloc_gemm_workspace(M, N, K)."""
+    M, K = _matrix_shape("a", a)
+    N = _matrix_shape("b", b)[0]
+    code = _type16(c, "c")
+    dev = _device(c, "c")
+    _check(LIB.qr_gemm_i8(
+        code, a.data_ptr(), _codes("a", a, M, K, dev), _vec("sa", sa, M, torch.float32, dev),
+        b.data_ptr(), _codes("b", b, N, K, dev), _vec("sb", sb, N, torch.float32, dev),
+        _vec("bias", bias, N, c.dtype, dev) if bias is not None else None, M, N, K,
+        c.data_ptr(), _mat("c", c, M, N, c.dtype, dev),
+        workspace.data_ptr() if workspace is not None else None,
+        _workspace_bytes(workspace, dev), _stream_on(dev, stream)))
+    return c
+
+
+def _workspace_bytes(t, dev):
+    if t is None:
+        return 0
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("workspace is not contiguous on GPU %d" % dev)
+    return _nbytes(t)
+
+
+def qr_gemm_i8_workspace_bytes(M, N, K):
+    return LIB.qr_gemm_i8_workspace_bytes(M, N, K)
+
+
+def alloc_gemm_workspace(M, N, K, device="cuda"):
+    """Device memory for qr_gemm_i8's workspace (None where it needs none)."""
+    n = qr_gemm_i8_workspace_bytes(M, N, K)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def alloc_q8(M, d, device="cuda"):
+    """Device buffers for M rows of d codes, each row starting at a multiple of
+    16 bytes as qr_gemm_i8 reads them, and for the M scales."""
+    q = torch.empty(M, -(-d // 16) * 16, dtype=torch.int8, device=device)[:, :d]
+    return q, torch.empty(M, dtype=torch.float32, device=device)
