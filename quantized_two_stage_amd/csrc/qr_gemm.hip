@@ -43,26 +43,29 @@ __device__ __forceinline__ i32x4 cut(i32x4 v, uint32_t k, uint32_t K) {
   return v;
 }
 
-// scales and bias of the W channels from n on
-template <int D, int W>
+// scales and bias of W neighbouring channels
+template <int W>
 struct Channels {
   float sb[W], bias[W];
   bool biased;
-  __device__ __forceinline__ Channels(const GemmArgs& g, uint32_t n) {
-    biased = g.bias != nullptr;
-    const uint16_t* b16 = reinterpret_cast<const uint16_t*>(g.bias);
-#pragma unroll
-    for (int e = 0; e < W; e++) {
-      const uint32_t at = n + e < g.N ? n + e : g.N - 1;
-      sb[e] = g.sb[at];
-      bias[e] = biased ? ld16<D>(b16[at]) : 0.0f;
-    }
-  }
   __device__ __forceinline__ float value(int32_t sum, float sa, int e) const {
     const float v = (float)sum * (sa * sb[e]);
     return biased ? v + bias[e] : v;
   }
 };
+template <int D, int W>
+__device__ __forceinline__ Channels<W> channels(const GemmArgs& g, uint32_t n) {
+  Channels<W> ch;
+  ch.biased = g.bias != nullptr;
+  const uint16_t* b16 = reinterpret_cast<const uint16_t*>(g.bias);
+#pragma unroll
+  for (int e = 0; e < W; e++) {
+    const uint32_t at = n + e < g.N ? n + e : g.N - 1;
+    ch.sb[e] = g.sb[at];
+    ch.bias[e] = ch.biased ? ld16<D>(b16[at]) : 0.0f;
+  }
+  return ch;
+}
 
 // W/2 words of 16-bit values to c[m][n..]: one store inside the row
 template <int W, class V>
@@ -71,9 +74,13 @@ __device__ __forceinline__ void store_row(const GemmArgs& g, uint32_t m, uint32_
   if (n + W <= g.N) {
     __builtin_memcpy(c, &w, 2 * W);
   } else {
+#pragma unroll 1
+    for (uint32_t e = 0; n + e < g.N; e++) {
+      uint32_t x = w[0];
 #pragma unroll
-    for (int e = 0; e < W; e++)
-      if (n + e < g.N) c[e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
+      for (uint32_t k = 1; k < W / 2; k++) x = e / 2 == k ? w[k] : x;
+      c[e] = (uint16_t)(x >> (16 * (e % 2)));
+    }
   }
 }
 
@@ -100,6 +107,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_tile(GemmArgs g, Grid gr) {
   constexpr int LA = BM * 8 / T, LB = BN * 8 / T;         // 16-byte pieces a lane loads a stage
   constexpr uint32_t kStage = (BM + BN) * 8;              // pieces of a stage
   __shared__ i32x4 lds[2 * kStage];
+  __shared__ float lsa[BM], lsb[BN], lbias[BN];
 
   const uint32_t t = threadIdx.x, lane = t % 64, wave = __builtin_amdgcn_readfirstlane(t / 64);
   uint32_t tm, tn;
@@ -188,6 +196,15 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_tile(GemmArgs g, Grid gr) {
     }
   };
 
+  // the scales and the bias, for the end
+  const uint16_t* bias = reinterpret_cast<const uint16_t*>(g.bias);
+  for (uint32_t x = t; x < BM; x += T) lsa[x] = g.sa[m0 + x < g.M ? m0 + x : g.M - 1];
+  for (uint32_t x = t; x < BN; x += T) {
+    const uint32_t n = n0 + x < g.N ? n0 + x : g.N - 1;
+    lsb[x] = g.sb[n];
+    lbias[x] = bias ? ld16<D>(bias[n]) : 0.0f;
+  }
+
   const i32x4 ra = buffer_at(pa, ~0u), rb = buffer_at(pb, ~0u);
   offsets(0);
 #pragma unroll
@@ -226,23 +243,30 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_tile(GemmArgs g, Grid gr) {
 
   // this lane holds, of token wm + 16i + p, the channels wn + 32(j/2) + 8q +
   // 4(j%2) + e: 8 neighbours for two j
+  float sa[FM];
+#pragma unroll
+  for (int i = 0; i < FM; i++) sa[i] = lsa[wm + 16 * i + p];
 #pragma unroll
   for (int j = 0; j < FN; j += 2) {
-    const uint32_t n = n0 + wn + 16 * j + 8 * q;
-    const Channels<D, 8> ch(g, n);
+    const uint32_t x = wn + 16 * j + 8 * q;
+    Channels<8> ch;
+    ch.biased = bias != nullptr;
+#pragma unroll
+    for (int e = 0; e < 8; e++) ch.sb[e] = lsb[x + e];
+#pragma unroll
+    for (int e = 0; e < 8; e++) ch.bias[e] = lbias[x + e];
 #pragma unroll
     for (int i = 0; i < FM; i++) {
       const uint32_t m = m0 + wm + 16 * i + p;
-      if (m >= g.M) continue;
-      const float sa = g.sa[m];
       u32x4 w;
 #pragma unroll
       for (int e = 0; e < 4; e += 2) {
-        w[e / 2] = st16x2<D>(ch.value(acc[i][j][e], sa, e), ch.value(acc[i][j][e + 1], sa, e + 1));
-        w[2 + e / 2] = st16x2<D>(ch.value(acc[i][j + 1][e], sa, 4 + e),
-                                 ch.value(acc[i][j + 1][e + 1], sa, 5 + e));
+        w[e / 2] = st16x2<D>(ch.value(acc[i][j][e], sa[i], e),
+                             ch.value(acc[i][j][e + 1], sa[i], e + 1));
+        w[2 + e / 2] = st16x2<D>(ch.value(acc[i][j + 1][e], sa[i], 4 + e),
+                                 ch.value(acc[i][j + 1][e + 1], sa[i], 5 + e));
       }
-      store_row<8>(g, m, n, w);
+      if (m < g.M) store_row<8>(g, m, n0 + x, w);
     }
   }
 }
@@ -318,7 +342,7 @@ __global__ __launch_bounds__(512) void k_few(GemmArgs g) {
 #pragma unroll
     for (int w = 1; w < W; w++) sum += part[w][f][x % 64];
     if (m < g.M && n < g.N) {
-      const Channels<D, 4> ch(g, n);
+      const Channels<4> ch = channels<D, 4>(g, n);
       const float sa = g.sa[m];
       u32x2 w;
 #pragma unroll
