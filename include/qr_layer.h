@@ -101,8 +101,9 @@ int qr_silu_mul_q8(qr_dtype dtype, const void* gu, size_t ldg, size_t M, size_t 
  * pieces of 16 bytes, so the bytes of a row up to the next multiple of 16
  * past K must be readable (the last row's too); what they hold does not
  * matter.  workspace: device memory of at least
- * qr_gemm_i8_workspace_bytes(M, N, K) bytes, 16-byte aligned (NULL where that
- * is 0); nothing in it needs to start at zero. */
+ * qr_gemm_i8_workspace_bytes(M, N, K) bytes.  That is 0 for every size in this
+ * version (partial sums stay on chip), so NULL will do and nothing is read
+ * from or written to it. */
 int qr_gemm_i8(qr_dtype dtype, const int8_t* a, size_t lda, const float* sa, const int8_t* b,
                size_t ldb, const float* sb, const void* bias, size_t M, size_t N, size_t K,
                void* c, size_t ldc, void* workspace, size_t ws_bytes, void* stream);

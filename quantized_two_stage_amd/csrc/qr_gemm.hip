@@ -1,5 +1,24 @@
 // qr_gemm.hip -- gfx950 kernels of qr_gemm_i8 (include/qr_layer.h): the matrix
 // product of 8-bit codes with a scale for each token and each output channel.
+//
+// c = (sum_k a[m][k] * b[n][k]) * (sa[m] * sb[n]) + bias[n]; the sum in 32-bit
+// integers on the matrix units (16x16x64 blocks), so any order of it gives
+// the same bits.  Both operands pass through LDS in stages of 128 codes,
+// loaded there directly (eight lanes to the 128 bytes of a row: read straight
+// into the matrix instructions' operands, where neighbouring lanes hold
+// different rows, the same bytes took one cycle a lane, 16 bytes a cycle and
+// CU).  Two kernels share the loads and the swizzle (16-byte piece c of row r
+// at place c ^ (r & 7): the 16 rows of a fragment fall on all banks):
+//   k_split  few tiles: the waves of a workgroup share the sum of one small
+//            tile, each with a ring of its own and no barrier; latency bounds
+//            a stage (0.065 us at 16x16, 0.24 us at 64x64), so the sum's
+//            stages run side by side;
+//   k_tile   many tiles: the waves share one tile and one ring; the matrix
+//            units and the loads bound it.
+// Measured (cold weights, bf16): 1 token over 8192x8192 weights 15.4 us, 4.4
+// TB/s of weights where a large copy reaches 5.2; 48 tokens, 8192x4096: 12.6
+// us; 8192^3: 435 us, 2530 TOPS (a library product of the same codes without
+// scales: 528 us).
 #include <type_traits>
 
 #include "qr.h"
@@ -26,11 +45,26 @@ __device__ __forceinline__ void load_to_lds(i32x4 rsrc, uint32_t lds, uint32_t v
       : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
       : "memory");
 }
-__device__ __forceinline__ i32x4 buffer_at(const void* p, uint32_t bytes) {
+// A buffer that starts at p, for load_to_lds.  The wait states are those that
+// a memory instruction needs after a vector instruction (readfirstlane) wrote
+// its scalar operands: the compiler does not see the loads in the assembly.
+// Later changes of a buffer are scalar instructions, which need none.
+__device__ __forceinline__ i32x4 buffer_at(const void* p) {
   const uint64_t a = (uint64_t)p;
   const int lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
   const int hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)) & 0xffff;
-  return i32x4{lo, hi, __builtin_amdgcn_readfirstlane((int)bytes), 0x00027000};
+  i32x4 r = {lo, hi, -1, 0x00027000};
+  asm volatile("s_nop 4" : "+s"(r));
+  return r;
+}
+// all of the buffer while s < steps, afterwards nothing (and nothing is fetched)
+__device__ __forceinline__ void end_buffer(i32x4& r, uint32_t s, uint32_t steps) {
+  int bytes;
+  asm("s_cmp_lt_u32 %1, %2\n\ts_cselect_b32 %0, -1, 0"
+      : "=s"(bytes)
+      : "s"(s), "s"(steps)
+      : "scc");
+  r[2] = bytes;
 }
 
 // The 16-byte piece v of a row, which starts at code k, with zeros past K.
@@ -100,13 +134,37 @@ __device__ __forceinline__ void tile_of(const Grid& gr, uint32_t b, uint32_t& m,
   n = r / rows;
 }
 
-template <int BM, int BN, int WM, int WN, int D>
+// The sums of W waves, each FN blocks of 16 channels wide and `Apart` entries
+// after the one before, joined and written: entry x holds 4 neighbouring
+// channels of one token.
+template <int D, int BM, int W, int FN, uint32_t Apart>
+__device__ __forceinline__ void finish(const GemmArgs& g, uint32_t m0, uint32_t n0, uint32_t x,
+                                       const i32x4* part) {
+  const uint32_t f = x / 64, m = m0 + f / FN * 16 + x % 16, n = n0 + f % FN * 16 + x % 64 / 16 * 4;
+  i32x4 sum = part[x];
+#pragma unroll
+  for (int w = 1; w < W; w++) sum += part[w * Apart + x];
+  if (m < g.M && n < g.N && (BM >= 16 || x % 16 < BM)) {
+    const Channels<4> ch = channels<D, 4>(g, n);
+    const float sa = g.sa[m];
+    u32x2 v;
+#pragma unroll
+    for (int e = 0; e < 4; e += 2)
+      v[e / 2] = st16x2<D>(ch.value(sum[e], sa, e), ch.value(sum[e + 1], sa, e + 1));
+    store_row<4>(g, m, n, v);
+  }
+}
+
+// A BM x BN tile to a workgroup of WM x WN waves, through a ring of S stages of
+// 128 codes.  S fills the LDS (S = 4 against 2 at 128x128: 38 us against 60 at
+// 1024x1024x8192; at 256x256 two stages are all that fit).
+template <int BM, int BN, int WM, int WN, int S, int D>
 __global__ __launch_bounds__(64 * WM * WN, 1) void k_tile(GemmArgs g, Grid gr) {
   constexpr int T = 64 * WM * WN;
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16;     // 16x16 blocks of a wave
   constexpr int LA = BM * 8 / T, LB = BN * 8 / T;         // 16-byte pieces a lane loads a stage
   constexpr uint32_t kStage = (BM + BN) * 8;              // pieces of a stage
-  __shared__ i32x4 lds[2 * kStage];
+  __shared__ i32x4 lds[S * kStage];
   __shared__ float lsa[BM], lsb[BN], lbias[BN];
 
   const uint32_t t = threadIdx.x, lane = t % 64, wave = __builtin_amdgcn_readfirstlane(t / 64);
@@ -144,19 +202,23 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_tile(GemmArgs g, Grid gr) {
   };
   // zeros for the codes of the last stage that lie past K (of a: the products
   // with whatever b holds there are then zero)
-  const auto cut_stage = [&](uint32_t parity) {
+  const auto cut_stage = [&](uint32_t at_stage) {
     const uint32_t k0 = (steps - 1) * kStep;
 #pragma unroll 1
     for (uint32_t x = t; x < BM * 8; x += T) {
       const uint32_t r = x / 8, k = k0 + 16 * (t % 8 ^ (r & 7));
-      i32x4* at = lds + parity * kStage + x;
+      i32x4* at = lds + at_stage + x;
       if (k + 16 > g.K) *at = cut(*at, k, g.K);
     }
     __syncthreads();
   };
-  const auto arrived = [] {                  // this wave's loads and LDS reads, then everyone's
+  // waits for all but this wave's youngest loads and its LDS reads, then everyone's
+  constexpr int kYoung = (S - 2) * (LA + LB);
+  static_assert(kYoung + LA + LB < 64, "s_waitcnt counts to 63");
+  const auto arrived = [](auto left) {
+    constexpr int n = decltype(left)::value;
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0070);
+    __builtin_amdgcn_s_waitcnt((n & 15) | (n >> 4) << 14 | 0x0070);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
@@ -205,38 +267,38 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_tile(GemmArgs g, Grid gr) {
     lbias[x] = bias ? ld16<D>(bias[n]) : 0.0f;
   }
 
-  const i32x4 ra = buffer_at(pa, ~0u), rb = buffer_at(pb, ~0u);
+  i32x4 ra = buffer_at(pa), rb = buffer_at(pb);
   offsets(0);
 #pragma unroll
-  for (int i = 0; i < LA + LB; i++) load(i, ra, rb, 0, 0);
-  arrived();
-  if (steps == 1 && cut_last) cut_stage(0);
-  if (steps > 1) {
-    if (steps == 2 && cut_last) offsets(kStep);
+  for (uint32_t s = 0; s < S; s++) {
+    if (s + 1 == steps && cut_last) offsets(s * kStep);
+    end_buffer(ra, s, steps);
+    end_buffer(rb, s, steps);
 #pragma unroll
-    for (int i = 0; i < LA + LB; i++) load(i, ra, rb, kStep, kStage * 16);
+    for (int i = 0; i < LA + LB; i++) load(i, ra, rb, s < steps ? s * kStep : 0u, s * kStage * 16);
   }
+  arrived(std::integral_constant<int, kYoung + LA + LB>{});
+  if (steps == 1 && cut_last) cut_stage(0);
 #pragma unroll
   for (int i = 0; i < FM + FN; i++) read(0, i);
 
   // One stage a turn.  Its second half is read while the first is multiplied;
   // then, with the next stage arrived and everyone done reading this one, the
-  // next one's first half is read and the stage after it loaded over this one,
-  // while the second half is multiplied.
-  uint32_t to = 0;                           // byte offset of this stage's buffer
+  // next one's first half is read and the stage S after this one loaded over
+  // it, while the second half is multiplied.
+  uint32_t to = 0;                           // this stage's place, in pieces
   for (uint32_t s = 0; s < steps; s++) {
     multiply(0, std::false_type{}, ra, rb, 0, 0);
-    arrived();
-    if (s + 2 == steps && cut_last) cut_stage(1 - s % 2);
-    if (s + 3 == steps && cut_last) offsets((s + 2) * kStep);
-    // past the last stage: an empty buffer, from which nothing is fetched
-    const bool more = s + 2 < steps;
-    const i32x4 ma = buffer_at(pa, more ? ~0u : 0u), mb = buffer_at(pb, more ? ~0u : 0u);
-    const uint32_t k = more ? (s + 2) * kStep : 0u;
-    xa = to ? xa - kStage : xa + kStage;
-    xb = to ? xb - kStage : xb + kStage;
-    multiply(1, std::true_type{}, ma, mb, k, to);
-    to = kStage * 16 - to;
+    arrived(std::integral_constant<int, kYoung>{});
+    const uint32_t next = to == (S - 1) * kStage ? 0 : to + kStage;
+    if (s + 2 == steps && cut_last) cut_stage(next);
+    if (s + 1 + S == steps && cut_last) offsets((s + S) * kStep);
+    end_buffer(ra, s + S, steps);
+    end_buffer(rb, s + S, steps);
+    xa += next - to;
+    xb += next - to;
+    multiply(1, std::true_type{}, ra, rb, s + S < steps ? (s + S) * kStep : 0u, to * 16);
+    to = next;
   }
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt(0x0f70);        // nothing may still be on its way to LDS
@@ -271,116 +333,172 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_tile(GemmArgs g, Grid gr) {
   }
 }
 
-// bytes [k, k+16) of a row, zeros past K; rows are readable up to K16
-__device__ __forceinline__ i32x4 load_cut(const int8_t* row, uint32_t k, uint32_t K) {
-  if (k >= K) return i32x4{0, 0, 0, 0};
-  return cut(*reinterpret_cast<const i32x4*>(row + k), k, K);
-}
-
-// M <= 16*MT tokens; a workgroup's eight waves share the sum of 16*NT channels
-template <int MT, int NT, int U, int D>
-__global__ __launch_bounds__(512) void k_few(GemmArgs g) {
-  constexpr int W = 8;
-  __shared__ i32x4 part[W][MT * NT][64];
+// A block of BM tokens by BN channels to a workgroup, whose W waves share the
+// sum: wave w takes stages w, w + W, ... through a ring of S stages of its own
+// in LDS, so the waves wait for nothing but their own loads until the end.
+template <int BM, int BN, int W, int S, int D>
+__global__ __launch_bounds__(64 * W) void k_split(GemmArgs g, Grid gr) {
+  constexpr int FM = (BM + 15) / 16, FN = BN / 16;
+  constexpr int LA = BM / 8, LB = BN / 8, L = LA + LB;    // loads of a stage
+  constexpr uint32_t kStage = (BM + BN) * 8;              // pieces of a stage
+  static_assert(FM * FN * 64 <= S * kStage && (S - 1) * L < 64);
+  __shared__ i32x4 lds[W * S * kStage];
   const uint32_t t = threadIdx.x, lane = t % 64, wave = __builtin_amdgcn_readfirstlane(t / 64);
-  const uint32_t p = lane % 16, q = lane / 16, n0 = blockIdx.x * 16 * NT;
-  const int8_t *pa[MT], *pb[NT];
+  uint32_t tm, tn;
+  tile_of(gr, blockIdx.x, tm, tn);
+  const uint32_t m0 = tm * BM, n0 = tn * BN;
+  const uint32_t K16 = (g.K + 15) & ~15u;
+  const uint32_t steps = (g.K + kStep - 1) / kStep;
+  const bool cut_last = g.K % kStep != 0;
+  const int8_t *pa = g.a + (size_t)m0 * g.lda, *pb = g.b + (size_t)n0 * g.ldb;
+  uint32_t va[LA], vb[LB];
+  const auto offsets = [&](uint32_t k) {
+    const uint32_t c = 16 * (lane % 8 ^ lane / 8), at = k + c < K16 ? c : K16 - 16 - k;
 #pragma unroll
-  for (int i = 0; i < MT; i++)
-    pa[i] = g.a + (size_t)(16 * i + p < g.M ? 16 * i + p : g.M - 1) * g.lda;
-#pragma unroll
-  for (int j = 0; j < NT; j++)
-    pb[j] = g.b + (size_t)(n0 + 16 * j + p < g.N ? n0 + 16 * j + p : g.N - 1) * g.ldb;
-  i32x4 acc[MT][NT] = {};
-  const uint32_t groups = g.K / (64 * U);
-  for (uint32_t s = wave; s < groups; s += W) {
-    i32x4 fa[U][MT], fb[U][NT];
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-      const uint32_t k = (s * U + u) * 64 + 16 * q;
-#pragma unroll
-      for (int j = 0; j < NT; j++)
-        fb[u][j] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(pb[j] + k));
+    for (int i = 0; i < LA; i++) {
+      const uint32_t r = i * 8 + lane / 8;
+      va[i] = (m0 + r < g.M ? r : g.M - 1 - m0) * (uint32_t)g.lda + at;
     }
 #pragma unroll
-    for (int u = 0; u < U; u++) {
-      const uint32_t k = (s * U + u) * 64 + 16 * q;
-#pragma unroll
-      for (int i = 0; i < MT; i++) fa[u][i] = *reinterpret_cast<const i32x4*>(pa[i] + k);
+    for (int i = 0; i < LB; i++) {
+      const uint32_t r = i * 8 + lane / 8;
+      vb[i] = (n0 + r < g.N ? r : g.N - 1 - n0) * (uint32_t)g.ldb + at;
     }
+  };
+  i32x4* const ring = lds + wave * S * kStage;
+  const uint32_t ring0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds +
+                         wave * S * kStage * 16;
+  i32x4 ra = buffer_at(pa), rb = buffer_at(pb);
+  // stage s into slot `to`; past the last stage from an empty buffer, from
+  // which nothing is fetched
+  const auto load = [&](uint32_t s, uint32_t to) {
+    const uint32_t k = s < steps ? s * kStep : 0u;
+    end_buffer(ra, s, steps);
+    end_buffer(rb, s, steps);
+    if (s + 1 == steps && cut_last) offsets(k);
 #pragma unroll
-    for (int u = 0; u < U; u++)
+    for (int i = 0; i < LB; i++) load_to_lds(rb, ring0 + (to * kStage + BM * 8 + i * 64) * 16, vb[i], k);
 #pragma unroll
-      for (int i = 0; i < MT; i++)
+    for (int i = 0; i < LA; i++) load_to_lds(ra, ring0 + (to * kStage + i * 64) * 16, va[i], k);
+  };
+  const uint32_t p = lane % 16, q = lane / 16;
+  const uint32_t x0 = p * 8 + (q ^ (p & 7)), xa = BM < 16 ? x0 & 63 : x0;
+  i32x4 acc[FM][FN] = {};
+  offsets(0);
 #pragma unroll
-        for (int j = 0; j < NT; j++)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[u][j], fa[u][i], acc[i][j], 0, 0, 0);
+  for (uint32_t i = 0; i < S; i++) load(wave + i * W, i);
+  uint32_t to = 0;
+#pragma unroll 1
+  for (uint32_t s = wave; s < steps; s += W) {
+    constexpr int n = (S - 1) * L;
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((n & 15) | (n >> 4) << 14 | 0x0f70);
+    asm volatile("" ::: "memory");
+    i32x4* const at = ring + to * kStage;
+    if (s + 1 == steps && cut_last) {
+      // zeros for the codes of a past K
+#pragma unroll
+      for (int i = 0; i < LA; i++) {
+        const uint32_t k = s * kStep + 16 * (lane % 8 ^ lane / 8);
+        if (k + 16 > g.K) at[i * 64 + lane] = cut(at[i * 64 + lane], k, g.K);
+      }
+    }
+    i32x4 fa[2][FM], fb[2][FN];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+#pragma unroll
+      for (int j = 0; j < FN; j++) fb[h][j] = at[BM * 8 + j * 128 + (x0 ^ (4 * h))];
+#pragma unroll
+      for (int i = 0; i < FM; i++) fa[h][i] = at[i * 128 + (xa ^ (4 * h))];
+    }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xc07f);      // the slot is read: it may be loaded again
+    asm volatile("" ::: "memory");
+    load(s + S * W, to);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+#pragma unroll
+      for (int i = 0; i < FM; i++)
+#pragma unroll
+        for (int j = 0; j < FN; j++)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[h][j], fa[h][i], acc[i][j], 0, 0, 0);
+    to = to + 1 == S ? 0 : to + 1;
   }
-  // at most U pieces of 64 codes are left, one to a wave
-  const uint32_t k0 = groups * U * 64 + wave * 64;
-  if (k0 < g.K) {
-    const uint32_t k = k0 + 16 * q;
-    i32x4 fa[MT], fb[NT];
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0f70);        // nothing may still be on its way to LDS
+  asm volatile("" ::: "memory");
 #pragma unroll
-    for (int j = 0; j < NT; j++) fb[j] = load_cut(pb[j], k, g.K);
+  for (int i = 0; i < FM; i++)
 #pragma unroll
-    for (int i = 0; i < MT; i++) fa[i] = load_cut(pa[i], k, g.K);
-#pragma unroll
-    for (int i = 0; i < MT; i++)
-#pragma unroll
-      for (int j = 0; j < NT; j++)
-        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
-  }
-#pragma unroll
-  for (int i = 0; i < MT; i++)
-#pragma unroll
-    for (int j = 0; j < NT; j++) part[wave][i * NT + j][lane] = acc[i][j];
+    for (int j = 0; j < FN; j++) ring[(i * FN + j) * 64 + lane] = acc[i][j];
   __syncthreads();
-  for (uint32_t x = t; x < MT * NT * 64; x += 512) {
-    const uint32_t f = x / 64, m = f / NT * 16 + x % 16, n = n0 + f % NT * 16 + x % 64 / 16 * 4;
-    i32x4 sum = part[0][f][x % 64];
-#pragma unroll
-    for (int w = 1; w < W; w++) sum += part[w][f][x % 64];
-    if (m < g.M && n < g.N) {
-      const Channels<4> ch = channels<D, 4>(g, n);
-      const float sa = g.sa[m];
-      u32x2 w;
-#pragma unroll
-      for (int e = 0; e < 4; e += 2)
-        w[e / 2] = st16x2<D>(ch.value(sum[e], sa, e), ch.value(sum[e + 1], sa, e + 1));
-      store_row<4>(g, m, n, w);
-    }
-  }
+  for (uint32_t x = t; x < FM * FN * 64; x += 64 * W) finish<D, BM, W, FN, S * kStage>(g, m0, n0, x, lds);
 }
 
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int W, int S>
+hipError_t split(int dtype, const GemmArgs& g, uint32_t group, hipStream_t st) {
+  const Grid gr{(g.M + BM - 1) / BM, (g.N + BN - 1) / BN, group};
+  const dim3 grid(gr.tm * gr.tn);
+  if (dtype == kF16) k_split<BM, BN, W, S, kF16><<<grid, 64 * W, 0, st>>>(g, gr);
+  else k_split<BM, BN, W, S, kBF16><<<grid, 64 * W, 0, st>>>(g, gr);
+  return hipGetLastError();
+}
+
+template <int BM, int BN, int WM, int WN, int S>
 hipError_t tiles(int dtype, const GemmArgs& g, uint32_t group, hipStream_t st) {
   const Grid gr{(g.M + BM - 1) / BM, (g.N + BN - 1) / BN, group};
   const dim3 grid(gr.tm * gr.tn), block(64 * WM * WN);
-  if (dtype == kF16) k_tile<BM, BN, WM, WN, kF16><<<grid, block, 0, st>>>(g, gr);
-  else k_tile<BM, BN, WM, WN, kBF16><<<grid, block, 0, st>>>(g, gr);
+  if (dtype == kF16) k_tile<BM, BN, WM, WN, S, kF16><<<grid, block, 0, st>>>(g, gr);
+  else k_tile<BM, BN, WM, WN, S, kBF16><<<grid, block, 0, st>>>(g, gr);
   return hipGetLastError();
 }
 
-template <int MT, int NT, int U>
-hipError_t few(int dtype, const GemmArgs& g, hipStream_t st) {
-  const dim3 grid((g.N + 16 * NT - 1) / (16 * NT));
-  if (dtype == kF16) k_few<MT, NT, U, kF16><<<grid, 512, 0, st>>>(g);
-  else k_few<MT, NT, U, kBF16><<<grid, 512, 0, st>>>(g);
-  return hipGetLastError();
-}
+// Tiles and what a workgroup of each was measured to take where every CU has
+// one at most: ns to start and end, and ns for each 128 codes of the sum.  The
+// launch takes the one whose rounds of 256 workgroups are estimated to end
+// first.  Measured at 1024 tokens x 1024 channels, K = 8192 (64 stages), us:
+// 32x32 of k_split 32 (four rounds), 64x64 of k_split 20.6, 64x64 of k_tile
+// 22.1, 128x128 38, 256x256 98; at 2048 x 16384, K = 4096: 126, 130 and more
+// for the first three, 128x128 190, 128x256 139, 256x256 132.  Against the
+// fastest of 40 tilings at each of 73 sizes the rule loses 3% at the median and
+// 22% (half a microsecond, 64x64x16) at most.
+struct Variant {
+  uint32_t bm, bn, fixed, stage;
+  hipError_t (*launch)(int, const GemmArgs&, uint32_t, hipStream_t);
+  uint32_t group;
+};
+constexpr Variant kVariants[] = {
+    {16, 16, 2800, 65, split<16, 16, 8, 2>, 16},
+    {16, 32, 2900, 100, split<16, 32, 4, 3>, 16},
+    {32, 32, 3100, 130, split<32, 32, 4, 2>, 16},
+    {64, 32, 4000, 190, split<64, 32, 4, 3>, 16},
+    {64, 64, 4500, 240, split<64, 64, 4, 2>, 16},
+    {64, 64, 3000, 290, tiles<64, 64, 2, 2, 4>, 8},
+    {128, 64, 3400, 380, tiles<128, 64, 4, 2, 5>, 8},
+    {128, 128, 4000, 520, tiles<128, 128, 2, 4, 4>, 8},
+    {128, 256, 4500, 780, tiles<128, 256, 2, 4, 3>, 8},
+    {256, 256, 5500, 1400, tiles<256, 256, 2, 4, 2>, 4},
+};
 
 }  // namespace
 
-size_t gemm_workspace_bytes(size_t, size_t, size_t) { return 0; }
-
 hipError_t launch_gemm(int dtype, const GemmArgs& g, hipStream_t st) {
-  if (g.M <= 16) return few<1, 1, 4>(dtype, g, st);
-  if (g.M <= 32) return few<2, 2, 4>(dtype, g, st);
-  if (g.M <= 64) return few<4, 2, 4>(dtype, g, st);
-  const size_t big = (size_t)((g.M + 255) / 256) * ((g.N + 255) / 256);
-  if (big >= 256) return tiles<256, 256, 2, 4>(dtype, g, 4, st);
-  return tiles<128, 128, 2, 2>(dtype, g, 8, st);
+  // up to 8 tokens only 8 rows of a are staged: 1 token, 8192x4096 9.5 us
+  // against 9.9 with 16 rows; 16384x1024 6.4 against 6.6 to 8.5
+  if (g.M <= 8) return split<8, 16, 4, 3>(dtype, g, 1, st);
+  const uint64_t steps = (g.K + kStep - 1) / kStep;
+  const Variant* best = nullptr;
+  uint64_t least = ~0ull;
+  for (const Variant& v : kVariants) {
+    const uint64_t blocks = (uint64_t)((g.M + v.bm - 1) / v.bm) * ((g.N + v.bn - 1) / v.bn);
+    const uint64_t ns = (blocks + 255) / 256 * (v.fixed + steps * v.stage);
+    if (ns < least) {
+      least = ns;
+      best = &v;
+    }
+  }
+  return best->launch(dtype, g, best->group, st);
 }
 
 }  // namespace qr

@@ -168,13 +168,12 @@ int qr_silu_mul_q8(qr_dtype dtype, const void* gu, size_t ldg, size_t M, size_t 
                     "activation launch");
 }
 
-size_t qr_gemm_i8_workspace_bytes(size_t M, size_t N, size_t K) {
-  return M == 0 || N == 0 || K == 0 ? 0 : qr::gemm_workspace_bytes(M, N, K);
-}
+// every size keeps its partial sums in LDS
+size_t qr_gemm_i8_workspace_bytes(size_t, size_t, size_t) { return 0; }
 
 int qr_gemm_i8(qr_dtype dtype, const int8_t* a, size_t lda, const float* sa, const int8_t* b,
                size_t ldb, const float* sb, const void* bias, size_t M, size_t N, size_t K,
-               void* c, size_t ldc, void* workspace, size_t ws_bytes, void* stream) {
+               void* c, size_t ldc, void* /*workspace*/, size_t /*ws_bytes*/, void* stream) {
   QR_TRY(check_dtype(dtype, false));
   if (K == 0 || K > QR_MAX_ROW)
     return fail(QR_ERR_SIZE, "K = %zu outside 1..%zu", K, QR_MAX_ROW);
@@ -203,18 +202,8 @@ int qr_gemm_i8(qr_dtype dtype, const int8_t* a, size_t lda, const float* sa, con
     QR_TRY(check(rbias));
     QR_TRY(check_apart(rc, rbias));
   }
-  const size_t need = qr::gemm_workspace_bytes(M, N, K);
-  if (need > 0) {
-    if (ws_bytes < need)
-      return fail(QR_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
-    const Rows ws{"workspace", workspace, 1, need, need, 1, 16};
-    QR_TRY(check(ws));
-    for (const Rows* r : {&ra, &rb, &rsa, &rsb, &rc}) QR_TRY(check_apart(ws, *r));
-    if (bias != nullptr) QR_TRY(check_apart(ws, rbias));
-  }
   const qr::GemmArgs g{a, lda, sa, b, ldb, sb, static_cast<const uint8_t*>(bias),
-                       static_cast<uint8_t*>(c), ldc, (uint32_t)M, (uint32_t)N, (uint32_t)K,
-                       static_cast<uint8_t*>(workspace)};
+                       static_cast<uint8_t*>(c), ldc, (uint32_t)M, (uint32_t)N, (uint32_t)K};
   (void)hipGetLastError();
   return hip_status(qr::launch_gemm(dtype, g, as_stream(stream)), "product launch");
 }

@@ -45,10 +45,8 @@ struct GemmArgs {
   uint8_t* c;
   size_t ldc;
   uint32_t M, N, K;
-  uint8_t* ws;
 };
 
-size_t gemm_workspace_bytes(size_t M, size_t N, size_t K);
 hipError_t launch_gemm(int dtype, const GemmArgs& g, hipStream_t st);
 
 }  // namespace qr
