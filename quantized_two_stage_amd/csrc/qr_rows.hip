@@ -10,6 +10,14 @@
 // reduction is enough rests on the norm's factor r being common to the row:
 // u_i*r*127/(a*r) = u_i*127/a, so the codes need the maximum a of u = h*weight
 // alone, and r enters the scale only.
+//
+// HBM bounds long batches: 8192 rows of 8192 (norm, bf16) take 89 us, 5.3 TB/s
+// (a large copy reaches 5.2); 4096 rows of 8192 from 4-bit wire codes 41 us,
+// 4.6 TB/s; the activation of 8192 rows of 4096 30 us, 5.5 TB/s.  Single rows
+// are bound by the latency of a launch, of one read and of the reduction:
+// 3.4 us at 8192 values.
+#include <type_traits>
+
 #include "qr.h"
 #include "qr_device.h"
 #include "qr_layer_internal.h"
@@ -58,12 +66,16 @@ __device__ __forceinline__ u32x4 load_each(const uint8_t* p, uint32_t n) {
   }
   return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
-template <bool Each>
+// rows that are whole vectors; rows whose last vector may be short; the same,
+// of any length
+enum Ends { kWhole, kShort, kAny };
+template <int E>
 __device__ __forceinline__ u32x4 load_vec(const uint8_t* p, uint32_t n) {
-  return Each ? load_each(p, n) : load_n(p, n);
+  return E == kWhole ? load8(p) : E == kShort ? load_n(p, n) : load_each(p, n);
 }
-__device__ __forceinline__ void store_n(uint8_t* p, u32x4 v, uint32_t n) {
-  if (n == 8) {
+template <int E>
+__device__ __forceinline__ void store_vec(uint8_t* p, u32x4 v, uint32_t n) {
+  if (E == kWhole || n == 8) {
     store8(p, v);
     return;
   }
@@ -120,7 +132,7 @@ constexpr int kBufType = D == kBF16H ? (int)kBF16 : D;
 // C < 0: x from 16-bit rows; else from the planar wire image of codec C.
 template <int D, int C>
 struct Norm {
-  static constexpr bool kNorm = true;
+  static constexpr bool kNorm = true, kWire = C >= 0;
   static constexpr int B = kBufType<D>;
   NormArgs a;
 
@@ -143,10 +155,10 @@ struct Norm {
     r.vec0 = C < 0 ? 0u : m * (d / 8);
     return r;
   }
-  template <bool Each>
+  template <int E>
   __device__ __forceinline__ void load(const Row& r, uint32_t vec, uint32_t n, Raw& v) const {
     if constexpr (C < 0) {
-      v.x = load_vec<Each>(r.x + 16 * (size_t)vec, n);
+      v.x = load_vec<E>(r.x + 16 * (size_t)vec, n);
     } else if constexpr (C == kFP) {
       v.x = load8(r.x + 16 * (size_t)(r.vec0 + vec));
     } else {
@@ -156,10 +168,11 @@ struct Norm {
       if constexpr (CodecT<C>::asym)
         v.z = reinterpret_cast<const uint16_t*>(r.x + a.off_z)[q >> 2];
     }
-    if (r.res) v.res = load_vec<Each>(r.res + 16 * (size_t)vec, n);
-    v.w = load_vec<Each>(a.weight + 16 * (size_t)vec, n);
+    if (r.res) v.res = load_vec<E>(r.res + 16 * (size_t)vec, n);
+    v.w = load_vec<E>(a.weight + 16 * (size_t)vec, n);
   }
   // u and the sum of squares, and h written
+  template <int E>
   __device__ __forceinline__ void values(const Row& r, uint32_t vec, uint32_t n, const Raw& v,
                                          float (&u)[8], float& ss) const {
     u32x4 h;
@@ -193,7 +206,7 @@ struct Norm {
         h[k] = st16x2<B>(hv[2 * k] + rv[2 * k], hv[2 * k + 1] + rv[2 * k + 1]);
       widen<B>(h, hv);
     }
-    if (r.h) store_n(r.h + 16 * (size_t)vec, h, n);
+    if (r.h) store_vec<E>(r.h + 16 * (size_t)vec, h, n);
     weigh(hv, v.w, u, ss);
   }
   __device__ __forceinline__ void weigh(const float (&hv)[8], u32x4 w, float (&u)[8],
@@ -207,13 +220,13 @@ struct Norm {
     }
   }
   // u of a vector whose h this lane has written (or x, where h is not)
-  template <bool Each>
+  template <int E>
   __device__ __forceinline__ void again(const Row& r, uint32_t vec, uint32_t n,
                                         float (&u)[8]) const {
     const uint8_t* p = (r.h ? r.h : r.x) + 16 * (size_t)vec;
     float hv[8], unused = 0.0f;
-    widen<B>(load_vec<Each>(p, n), hv);
-    weigh(hv, load_vec<Each>(a.weight + 16 * (size_t)vec, n), u, unused);
+    widen<B>(load_vec<E>(p, n), hv);
+    weigh(hv, load_vec<E>(a.weight + 16 * (size_t)vec, n), u, unused);
   }
   __device__ __forceinline__ float factor(float ss, uint32_t d) const {
     return 1.0f / __builtin_sqrtf(ss / (float)d + a.eps);
@@ -222,7 +235,7 @@ struct Norm {
 
 template <int D>
 struct Silu {
-  static constexpr bool kNorm = false;
+  static constexpr bool kNorm = false, kWire = false;
   const uint8_t* gu;
   size_t ldg;
 
@@ -236,15 +249,16 @@ struct Silu {
     const uint8_t* p = gu + 2 * (size_t)m * ldg;
     return Row{p, p + 2 * (size_t)d};
   }
-  template <bool Each>
+  template <int E>
   __device__ __forceinline__ void load(const Row& r, uint32_t vec, uint32_t n, Raw& v) const {
-    v.g = load_vec<Each>(r.g + 16 * (size_t)vec, n);
-    v.u = load_vec<Each>(r.u + 16 * (size_t)vec, n);
+    v.g = load_vec<E>(r.g + 16 * (size_t)vec, n);
+    v.u = load_vec<E>(r.u + 16 * (size_t)vec, n);
   }
   // g / (1 + exp(-g)) * u.  exp by v_exp_f32 (2^x): the rounding of the
   // exponent costs |g| * 2^-24 relative to exp(-g), which matters only where
   // exp(-g) is large, that is where the value is near zero; v_rcp_f32 is
   // within one unit in the last place.  exp(-g) = inf gives g * 0.
+  template <int E>
   __device__ __forceinline__ void values(const Row&, uint32_t, uint32_t, const Raw& v,
                                          float (&u)[8], float&) const {
     float g[8];
@@ -256,51 +270,72 @@ struct Silu {
       u[i] = g[i] * __builtin_amdgcn_rcpf(1.0f + e) * u[i];
     }
   }
-  template <bool Each>
+  template <int E>
   __device__ __forceinline__ void again(const Row& r, uint32_t vec, uint32_t n,
                                         float (&u)[8]) const {
     Raw v;
     float unused;
-    load<Each>(r, vec, n, v);
-    values(r, vec, n, v, u, unused);
+    load<E>(r, vec, n, v);
+    values<E>(r, vec, n, v, u, unused);
   }
   __device__ __forceinline__ float factor(float, uint32_t) const { return 1.0f; }
 };
 
 // ---------------------------------------------------------------------------
 
+// v joined over the wave by `join`, the same bits in every lane: exchanges
+// inside a row of 16 lanes, then of rows and of halves
+template <class Join>
+__device__ __forceinline__ float wave_join(float v, Join join) {
+  const auto dpp = [](float x, auto ctrl) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), decltype(ctrl)::value, 0xf,
+                                        0xf, true));
+  };
+  v = join(v, dpp(v, std::integral_constant<int, 0xb1>{}));      // lane ^ 1
+  v = join(v, dpp(v, std::integral_constant<int, 0x4e>{}));      // lane ^ 2
+  v = join(v, dpp(v, std::integral_constant<int, 0x141>{}));     // the other four of 8
+  v = join(v, dpp(v, std::integral_constant<int, 0x140>{}));     // the other eight of 16
+  const uint32_t x = __builtin_bit_cast(uint32_t, v);
+  const auto rows = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  v = join(__builtin_bit_cast(float, (uint32_t)rows[0]), __builtin_bit_cast(float, (uint32_t)rows[1]));
+  const uint32_t y = __builtin_bit_cast(uint32_t, v);
+  const auto halves = __builtin_amdgcn_permlane32_swap(y, y, false, false);
+  return join(__builtin_bit_cast(float, (uint32_t)halves[0]),
+              __builtin_bit_cast(float, (uint32_t)halves[1]));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
-  return v;
+  return wave_join(v, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int m = 32; m > 0; m >>= 1) v = __builtin_elementwise_maximum(v, __shfl_xor(v, m));
-  return v;
+  return wave_join(v, [](float a, float b) { return __builtin_elementwise_maximum(a, b); });
 }
 
-// over the T lanes of a row; T > 64: through LDS, every lane gets the result
-template <int T, bool Sum>
-__device__ __forceinline__ void row_reduce(float& ss, float& a, float* lds) {
-  if (Sum) ss = wave_sum(ss);
-  a = wave_max(a);
-  if constexpr (T > 64) {
-    constexpr int nw = T / 64;
-    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
-    if (lane == 0) {
-      if (Sum) lds[wave] = ss;
-      lds[nw + wave] = a;
-    }
-    __syncthreads();
-    ss = 0.0f;
-    a = 0.0f;
-#pragma unroll
-    for (int w = 0; w < nw; w++) {
-      if (Sum) ss += lds[w];
-      a = __builtin_elementwise_maximum(a, lds[nw + w]);
-    }
+// over the row's waves, at most 16, through LDS: every lane gets the result.
+// Entries of waves that are not there hold 0, which changes neither (magnitudes
+// are not negative).
+struct Joined {
+  float ss[16], a[16];
+};
+template <bool Sum>
+__device__ __forceinline__ void waves_reduce(float& ss, float& a, Joined& lds) {
+  const uint32_t t = threadIdx.x;
+  if (t % 64 == 0) {
+    if (Sum) lds.ss[t / 64] = ss;
+    lds.a[t / 64] = a;
   }
+  __syncthreads();
+  ss = 0.0f;
+  a = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 16; w++) {
+    if (Sum) ss += lds.ss[w];
+    a = __builtin_elementwise_maximum(a, lds.a[w]);
+  }
+}
+__device__ __forceinline__ void clear(Joined& lds) {
+  const uint32_t t = threadIdx.x, waves = blockDim.x / 64;
+  if (t >= waves && t < 16) lds.ss[t] = lds.a[t] = 0.0f;
 }
 
 // 8 codes; f = 0 marks a row without codes
@@ -319,8 +354,9 @@ __device__ __forceinline__ u32x2 code8(const float (&u)[8], float f) {
   }
   return w;
 }
+template <int E>
 __device__ __forceinline__ void store_codes(int8_t* p, u32x2 w, uint32_t n) {
-  if (n == 8) {
+  if (E == kWhole || n == 8) {
     __builtin_memcpy(p, &w, 8);
   } else {
     const uint64_t v = w.x | (uint64_t)w.y << 32;
@@ -341,44 +377,53 @@ __device__ __forceinline__ float row_scale(const Op& op, float ss, float a, uint
   return use ? 127.0f / a : 0.0f;
 }
 
-constexpr int rows_per_group(int T) { return T == 64 ? 4 : 1; }
+constexpr uint32_t kRowsOfAGroup = 4;              // where a row has one wave
 
-// T lanes to a row of at most 8*T*V values, held in registers
-template <class Op, int T, int V>
-__global__ __launch_bounds__(T * rows_per_group(T)) void k_rows(Op op, RowsOut o) {
-  constexpr int R = rows_per_group(T);
-  __shared__ float lds[2 * (T / 64)];
-  const uint32_t t = threadIdx.x % T;
-  for (uint32_t m = blockIdx.x * R + threadIdx.x / T; m < o.M; m += gridDim.x * R) {
+// A row of at most 8*V values a lane, held in registers.  Wave: a wave to a
+// row, kRowsOfAGroup of them to a workgroup; else the workgroup's lanes to a row.
+template <class Op, bool Wave, int V, int E>
+__global__ __launch_bounds__(Wave ? 64 * kRowsOfAGroup : 1024) void k_rows(Op op, RowsOut o) {
+  __shared__ Joined lds;
+  const uint32_t R = Wave ? kRowsOfAGroup : 1, T = Wave ? 64 : blockDim.x;
+  const uint32_t t = Wave ? threadIdx.x % 64 : threadIdx.x;
+  if (!Wave) clear(lds);
+  for (uint32_t m = blockIdx.x * R + (Wave ? threadIdx.x / 64 : 0); m < o.M; m += gridDim.x * R) {
     const auto row = op.row(m, o.d);
-    typename Op::Raw raw[V];
+    constexpr int B = V < 2 ? V : 2;       // vectors on their way at a time
     float u[V][8];
     float ss = 0.0f, a = 0.0f;
 #pragma unroll
-    for (int j = 0; j < V; j++) {
-      const uint32_t i0 = 8 * (t + T * j);
-      if (i0 < o.d) op.template load<false>(row, t + T * j, o.d - i0 < 8 ? o.d - i0 : 8, raw[j]);
-    }
+    for (int j0 = 0; j0 < V; j0 += B) {
+      typename Op::Raw raw[B];
 #pragma unroll
-    for (int j = 0; j < V; j++) {
-      const uint32_t i0 = 8 * (t + T * j);
-      if (i0 < o.d) {
-        op.values(row, t + T * j, o.d - i0 < 8 ? o.d - i0 : 8, raw[j], u[j], ss);
-#pragma unroll
-        for (int i = 0; i < 8; i++) a = max_abs(a, u[j][i]);
+      for (int j = 0; j < B; j++) {
+        const uint32_t vec = t + T * (j0 + j), i0 = 8 * vec;
+        if (i0 < o.d) op.template load<E>(row, vec, o.d - i0 < 8 ? o.d - i0 : 8, raw[j]);
       }
+#pragma unroll
+      for (int j = 0; j < B; j++) {
+        const uint32_t vec = t + T * (j0 + j), i0 = 8 * vec;
+        if (i0 < o.d) {
+          op.template values<E>(row, vec, o.d - i0 < 8 ? o.d - i0 : 8, raw[j], u[j0 + j], ss);
+#pragma unroll
+          for (int i = 0; i < 8; i++) a = max_abs(a, u[j0 + j][i]);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    row_reduce<T, Op::kNorm>(ss, a, lds);
+    if (Op::kNorm) ss = wave_sum(ss);
+    a = wave_max(a);
+    if (!Wave) waves_reduce<Op::kNorm>(ss, a, lds);
     float scale;
     const float f = row_scale(op, ss, a, o.d, scale);
     int8_t* q = o.q + (size_t)m * o.ldq;
 #pragma unroll
     for (int j = 0; j < V; j++) {
       const uint32_t i0 = 8 * (t + T * j);
-      if (i0 < o.d) store_codes(q + i0, code8(u[j], f), o.d - i0 < 8 ? o.d - i0 : 8);
+      if (i0 < o.d) store_codes<E>(q + i0, code8(u[j], f), o.d - i0 < 8 ? o.d - i0 : 8);
     }
     if (t == 0) o.scales[m] = scale;
-    if (T > 64 && m + gridDim.x < o.M) __syncthreads();       // lds is used again
+    if (!Wave && m + gridDim.x < o.M) __syncthreads();         // lds is used again
   }
 }
 
@@ -386,7 +431,8 @@ __global__ __launch_bounds__(T * rows_per_group(T)) void k_rows(Op op, RowsOut o
 // what it has itself written or read)
 template <class Op, int T>
 __global__ __launch_bounds__(T) void k_rows_long(Op op, RowsOut o) {
-  __shared__ float lds[2 * (T / 64)];
+  __shared__ Joined lds;
+  clear(lds);
   for (uint32_t m = blockIdx.x; m < o.M; m += gridDim.x) {
     const auto row = op.row(m, o.d);
     float ss = 0.0f, a = 0.0f;
@@ -394,44 +440,67 @@ __global__ __launch_bounds__(T) void k_rows_long(Op op, RowsOut o) {
       const uint32_t n = o.d - 8 * vec < 8 ? o.d - 8 * vec : 8;
       typename Op::Raw raw;
       float u[8];
-      op.template load<true>(row, vec, n, raw);
-      op.values(row, vec, n, raw, u, ss);
+      op.template load<kAny>(row, vec, n, raw);
+      op.template values<kAny>(row, vec, n, raw, u, ss);
 #pragma unroll
       for (int i = 0; i < 8; i++) a = max_abs(a, u[i]);
     }
-    row_reduce<T, Op::kNorm>(ss, a, lds);
+    if (Op::kNorm) ss = wave_sum(ss);
+    a = wave_max(a);
+    waves_reduce<Op::kNorm>(ss, a, lds);
     float scale;
     const float f = row_scale(op, ss, a, o.d, scale);
     int8_t* q = o.q + (size_t)m * o.ldq;
     for (uint32_t vec = threadIdx.x; 8 * vec < o.d; vec += T) {
       const uint32_t n = o.d - 8 * vec < 8 ? o.d - 8 * vec : 8;
       float u[8];
-      op.template again<true>(row, vec, n, u);
-      store_codes(q + 8 * vec, code8(u, f), n);
+      op.template again<kAny>(row, vec, n, u);
+      store_codes<kAny>(q + 8 * vec, code8(u, f), n);
     }
     if (threadIdx.x == 0) o.scales[m] = scale;
     if (m + gridDim.x < o.M) __syncthreads();
   }
 }
 
+constexpr uint32_t kMaxGroups = 1u << 21;         // times 1024 lanes: below 2^32
+
+template <class Op, bool Wave, int V, int E>
+hipError_t rows_in_registers(const Op& op, const RowsOut& o, hipStream_t st) {
+  constexpr uint32_t R = Wave ? kRowsOfAGroup : 1;
+  const uint32_t g = (o.M + R - 1) / R, lanes = (o.d + 8 * V - 1) / (8 * V);
+  k_rows<Op, Wave, V, E><<<g < kMaxGroups ? g : kMaxGroups, Wave ? 64 * R : (lanes + 63) / 64 * 64,
+                           0, st>>>(op, o);
+  return hipGetLastError();
+}
+template <class Op, int T>
+hipError_t rows_twice(const Op& op, const RowsOut& o, hipStream_t st) {
+  k_rows_long<Op, T><<<o.M < kMaxGroups ? o.M : kMaxGroups, T, 0, st>>>(op, o);
+  return hipGetLastError();
+}
+
+// One vector to a lane wherever a workgroup has the lanes, and no more waves
+// than the row needs: the loads of a row are all on their way at once, few
+// registers are held, and many waves share a CU.  The norm from 16-bit rows,
+// us: 8192 rows of 8192 with 1024 lanes x 1 vector 89, 512 x 2 88, 256 x 4 98,
+// 128 x 8 117; of 4096 with 512 x 1 45, 256 x 2 48, 1024 x 1 56; one row of 8192
+// 3.4, 3.4, 4.2, 5.9; 1024 rows of 5003 with 640 lanes 14.4, with 1024 lanes
+// 19.9.  Rows that are whole vectors apart from the others: the former with
+// the latter's loads take 113 instead of 98 (256 x 4).
+template <class Op, int E>
+hipError_t rows_by_length(const Op& op, const RowsOut& o, hipStream_t st) {
+  if (o.d <= 512) return rows_in_registers<Op, true, 1, E>(op, o, st);
+  if (o.d <= 8192) return rows_in_registers<Op, false, 1, E>(op, o, st);
+  if (o.d <= 16384) return rows_in_registers<Op, false, 2, E>(op, o, st);
+  if (o.d <= 32768) return rows_in_registers<Op, false, 4, E>(op, o, st);
+  return rows_twice<Op, 1024>(op, o, st);
+}
 template <class Op>
 hipError_t launch_rows(const Op& op, const RowsOut& o, hipStream_t st) {
-  constexpr uint32_t kMaxGroups = 1u << 21;       // times 1024 lanes: below 2^32
-  const auto groups = [&](uint32_t R) {
-    const uint32_t g = (o.M + R - 1) / R;
-    return dim3(g < kMaxGroups ? g : kMaxGroups);
-  };
-  if (o.d < 8)
-    k_rows_long<Op, 64><<<groups(1), 64, 0, st>>>(op, o);
-  else if (o.d <= 2048)
-    k_rows<Op, 64, 4><<<groups(4), 256, 0, st>>>(op, o);
-  else if (o.d <= 8192)
-    k_rows<Op, 256, 4><<<groups(1), 256, 0, st>>>(op, o);
-  else if (o.d <= 32768)
-    k_rows<Op, 1024, 4><<<groups(1), 1024, 0, st>>>(op, o);
-  else
-    k_rows_long<Op, 1024><<<groups(1), 1024, 0, st>>>(op, o);
-  return hipGetLastError();
+  if constexpr (!Op::kWire) {            // a wire image's rows are whole vectors
+    if (o.d < 8) return rows_twice<Op, 64>(op, o, st);
+    if (o.d % 8 != 0) return rows_by_length<Op, kShort>(op, o, st);
+  }
+  return rows_by_length<Op, kWhole>(op, o, st);
 }
 
 template <int D>
