@@ -273,14 +273,19 @@ def _type16(t, what):
     return code
 
 
-def _mat(what, t, rows, cols, dtype, dev):
-    """A matrix argument: its row stride in elements (rows contiguous)."""
+def _refuse(what, t, dtype, dev, shape):
     if t.dtype is not dtype:
         raise TypeError("%s is %s: %s expected" % (what, t.dtype, dtype))
-    if t.shape != (rows, cols):
-        raise ValueError("%s has shape %s: %s expected" % (what, tuple(t.shape), (rows, cols)))
     if t.get_device() != dev:
         raise ValueError("%s is not on GPU %d" % (what, dev))
+    raise ValueError(shape)
+
+
+def _mat(what, t, rows, cols, dtype, dev):
+    """A matrix argument: its row stride in elements (rows contiguous)."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != (rows, cols):
+        _refuse(what, t, dtype, dev,
+                "%s has shape %s: %s expected" % (what, tuple(t.shape), (rows, cols)))
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError("%s: the values of a row are not contiguous" % what)
@@ -288,12 +293,8 @@ def _mat(what, t, rows, cols, dtype, dev):
 
 
 def _vec(what, t, n, dtype, dev):
-    if t.dtype is not dtype:
-        raise TypeError("%s is %s: %s expected" % (what, t.dtype, dtype))
-    if t.numel() != n:
-        raise ValueError("%s holds %d values: %d expected" % (what, t.numel(), n))
-    if t.get_device() != dev:
-        raise ValueError("%s is not on GPU %d" % (what, dev))
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() != n:
+        _refuse(what, t, dtype, dev, "%s holds %d values: %d expected" % (what, t.numel(), n))
     if not t.is_contiguous():
         raise ValueError("%s is not contiguous" % what)
     return t.data_ptr()
@@ -305,8 +306,8 @@ def _codes(what, t, rows, cols, dev):
     ld = _mat(what, t, rows, cols, torch.int8, dev)
     if rows == 1:
         ld = -(-ld // 16) * 16
-    if rows > 0 and (t.storage_offset() + (rows - 1) * ld + -(-cols // 16) * 16
-                     > t.untyped_storage().nbytes()):
+    if cols % 16 and rows > 0 and (t.storage_offset() + (rows - 1) * ld + -(-cols // 16) * 16
+                                   > t.untyped_storage().nbytes()):
         raise ValueError("%s: the padding of its last row up to a multiple of 16 is outside "
                          "its storage (alloc_q8 makes room for it)" % what)
     return ld
@@ -315,7 +316,7 @@ def _codes(what, t, rows, cols, dev):
 def _device(t, what):
     """The current GPU, which the tensors of a call must be on."""
     dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError("%s is not on the current GPU" % what)
     return dev
 
