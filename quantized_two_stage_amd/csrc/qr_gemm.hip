@@ -15,8 +15,8 @@
 //            stages run side by side;
 //   k_tile   many tiles: the waves share one tile and one ring; the matrix
 //            units and the loads bound it.
-// Measured (cold weights, bf16): 1 token over 8192x8192 weights 15.4 us, 4.4
-// TB/s of weights where a large copy reaches 5.2; 48 tokens, 8192x4096: 12.6
+// Measured (cold weights, bf16): 1 token over 8192x8192 weights 13.1 us, 5.1
+// TB/s of weights where a large copy reaches 5.2; 48 tokens, 8192x4096: 11.9
 // us; 8192^3: 435 us, 2530 TOPS (a library product of the same codes without
 // scales: 528 us).
 #include <type_traits>
@@ -37,13 +37,22 @@ constexpr uint32_t kStep = 128;       // codes of the sum in one stage of the ti
 // assembly since the compiler, where it cannot tell two LDS buffers apart,
 // would wait for the load before any LDS read: the caller waits.  It has no
 // output register, so nothing is written behind the compiler's back but LDS.
+// Once: past the caches, for what no other workgroup reads.
+template <bool Once>
 __device__ __forceinline__ void load_to_lds(i32x4 rsrc, uint32_t lds, uint32_t voff,
                                             uint32_t soff) {
-  asm volatile(
-      "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-      :
-      : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
-      : "memory");
+  if constexpr (Once)
+    asm volatile(
+        "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+        :
+        : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+        : "memory");
+  else
+    asm volatile(
+        "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+        :
+        : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+        : "memory");
 }
 // A buffer that starts at p, for load_to_lds.  The wait states are those that
 // a memory instruction needs after a vector instruction (readfirstlane) wrote
@@ -158,7 +167,7 @@ __device__ __forceinline__ void finish(const GemmArgs& g, uint32_t m0, uint32_t 
 // A BM x BN tile to a workgroup of WM x WN waves, through a ring of S stages of
 // 128 codes.  S fills the LDS (S = 4 against 2 at 128x128: 38 us against 60 at
 // 1024x1024x8192; at 256x256 two stages are all that fit).
-template <int BM, int BN, int WM, int WN, int S, int D>
+template <int BM, int BN, int WM, int WN, int S, int D, bool Once>
 __global__ __launch_bounds__(64 * WM * WN, 1) void k_tile(GemmArgs g, Grid gr) {
   constexpr int T = 64 * WM * WN;
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16;     // 16x16 blocks of a wave
@@ -197,8 +206,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_tile(GemmArgs g, Grid gr) {
                         wave * 1024;
   // piece-loads 0..LA+LB-1 of the stage at code k into the buffer at byte `to`
   const auto load = [&](int i, i32x4 ra, i32x4 rb, uint32_t k, uint32_t to) {
-    if (i < LA) load_to_lds(ra, lds0 + to + i * T * 16, va[i < LA ? i : 0], k);
-    else load_to_lds(rb, lds0 + to + (BM * 8 + (i - LA) * T) * 16, vb[i < LA ? 0 : i - LA], k);
+    if (i < LA) load_to_lds<false>(ra, lds0 + to + i * T * 16, va[i < LA ? i : 0], k);
+    else load_to_lds<Once>(rb, lds0 + to + (BM * 8 + (i - LA) * T) * 16, vb[i < LA ? 0 : i - LA], k);
   };
   // zeros for the codes of the last stage that lie past K (of a: the products
   // with whatever b holds there are then zero)
@@ -336,7 +345,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_tile(GemmArgs g, Grid gr) {
 // A block of BM tokens by BN channels to a workgroup, whose W waves share the
 // sum: wave w takes stages w, w + W, ... through a ring of S stages of its own
 // in LDS, so the waves wait for nothing but their own loads until the end.
-template <int BM, int BN, int W, int S, int D>
+template <int BM, int BN, int W, int S, int D, bool Once>
 __global__ __launch_bounds__(64 * W) void k_split(GemmArgs g, Grid gr) {
   constexpr int FM = (BM + 15) / 16, FN = BN / 16;
   constexpr int LA = BM / 8, LB = BN / 8, L = LA + LB;    // loads of a stage
@@ -377,9 +386,11 @@ __global__ __launch_bounds__(64 * W) void k_split(GemmArgs g, Grid gr) {
     end_buffer(rb, s, steps);
     if (s + 1 == steps && cut_last) offsets(k);
 #pragma unroll
-    for (int i = 0; i < LB; i++) load_to_lds(rb, ring0 + (to * kStage + BM * 8 + i * 64) * 16, vb[i], k);
+    for (int i = 0; i < LB; i++)
+      load_to_lds<Once>(rb, ring0 + (to * kStage + BM * 8 + i * 64) * 16, vb[i], k);
 #pragma unroll
-    for (int i = 0; i < LA; i++) load_to_lds(ra, ring0 + (to * kStage + i * 64) * 16, va[i], k);
+    for (int i = 0; i < LA; i++)
+      load_to_lds<false>(ra, ring0 + (to * kStage + i * 64) * 16, va[i], k);
   };
   const uint32_t p = lane % 16, q = lane / 16;
   const uint32_t x0 = p * 8 + (q ^ (p & 7)), xa = BM < 16 ? x0 & 63 : x0;
@@ -436,21 +447,35 @@ __global__ __launch_bounds__(64 * W) void k_split(GemmArgs g, Grid gr) {
   for (uint32_t x = t; x < FM * FN * 64; x += 64 * W) finish<D, BM, W, FN, S * kStage>(g, m0, n0, x, lds);
 }
 
-template <int BM, int BN, int W, int S>
-hipError_t split(int dtype, const GemmArgs& g, uint32_t group, hipStream_t st) {
-  const Grid gr{(g.M + BM - 1) / BM, (g.N + BN - 1) / BN, group};
-  const dim3 grid(gr.tm * gr.tn);
-  if (dtype == kF16) k_split<BM, BN, W, S, kF16><<<grid, 64 * W, 0, st>>>(g, gr);
-  else k_split<BM, BN, W, S, kBF16><<<grid, 64 * W, 0, st>>>(g, gr);
-  return hipGetLastError();
-}
-
+// Weights that one row of tiles covers are read by one workgroup only, and a
+// model's weights do not stay in the 256 MB cache until they are used again:
+// past the caches, one token over cold 8192x8192 weights takes 13.1 us instead
+// of 15.4, 8192x4096 8.3 instead of 9.5, 48 tokens 11.9 instead of 12.6.  Where
+// the same 67 MB are read again and again it costs 12.3 against 11.5.
 template <int BM, int BN, int WM, int WN, int S>
 hipError_t tiles(int dtype, const GemmArgs& g, uint32_t group, hipStream_t st) {
   const Grid gr{(g.M + BM - 1) / BM, (g.N + BN - 1) / BN, group};
   const dim3 grid(gr.tm * gr.tn), block(64 * WM * WN);
-  if (dtype == kF16) k_tile<BM, BN, WM, WN, S, kF16><<<grid, block, 0, st>>>(g, gr);
-  else k_tile<BM, BN, WM, WN, S, kBF16><<<grid, block, 0, st>>>(g, gr);
+  const auto kernel = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    if (gr.tm == 1) k_tile<BM, BN, WM, WN, S, D, true><<<grid, block, 0, st>>>(g, gr);
+    else k_tile<BM, BN, WM, WN, S, D, false><<<grid, block, 0, st>>>(g, gr);
+  };
+  if (dtype == kF16) kernel(std::integral_constant<int, kF16>{});
+  else kernel(std::integral_constant<int, kBF16>{});
+  return hipGetLastError();
+}
+template <int BM, int BN, int W, int S>
+hipError_t split(int dtype, const GemmArgs& g, uint32_t group, hipStream_t st) {
+  const Grid gr{(g.M + BM - 1) / BM, (g.N + BN - 1) / BN, group};
+  const dim3 grid(gr.tm * gr.tn), block(64 * W);
+  const auto kernel = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    if (gr.tm == 1) k_split<BM, BN, W, S, D, true><<<grid, block, 0, st>>>(g, gr);
+    else k_split<BM, BN, W, S, D, false><<<grid, block, 0, st>>>(g, gr);
+  };
+  if (dtype == kF16) kernel(std::integral_constant<int, kF16>{});
+  else kernel(std::integral_constant<int, kBF16>{});
   return hipGetLastError();
 }
 
@@ -484,8 +509,8 @@ constexpr Variant kVariants[] = {
 }  // namespace
 
 hipError_t launch_gemm(int dtype, const GemmArgs& g, hipStream_t st) {
-  // up to 8 tokens only 8 rows of a are staged: 1 token, 8192x4096 9.5 us
-  // against 9.9 with 16 rows; 16384x1024 6.4 against 6.6 to 8.5
+  // up to 8 tokens only 8 rows of a are staged: 1 token, 2048x8192 7.1 us
+  // against 8.8 (16x32) with 16 rows; 16384x1024 6.4 against 6.6
   if (g.M <= 8) return split<8, 16, 4, 3>(dtype, g, 1, st);
   const uint64_t steps = (g.K + kStep - 1) / kStep;
   const Variant* best = nullptr;
