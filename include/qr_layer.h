@@ -16,10 +16,10 @@
  * 8-bit rows.  A matrix of M rows ("tokens") of d values is held as M rows of
  * int8 codes and M binary32 scales; row m stands for code * scales[m].  The
  * codes of a row u (binary32 values) are
- *     a = max |u_i|;  code_i = round-half-even(u_i * f), f = 127 / a
- * with f and the product each rounded once to binary32, so |code_i| <= 127
- * and the largest value has code +-127.  A row with a < 2^-119 (where f would
- * overflow; all zeros among them) has codes 0 and scale 0.  A row that holds
+ *     a = max |u_i|;  code_i = round-half-even(127 * u_i / a)
+ * of the exact quotient, so |code_i| <= 127 and the largest value has code
+ * +-127.  A row with a < 2^-119 (where 127 / a would overflow; all zeros among
+ * them) has codes 0 and scale 0.  A row that holds
  * a NaN or an infinity has codes 0 and scale NaN, so that every product with
  * it is NaN.
  *

@@ -254,10 +254,11 @@ struct Silu {
     v.g = load_vec<E>(r.g + 16 * (size_t)vec, n);
     v.u = load_vec<E>(r.u + 16 * (size_t)vec, n);
   }
-  // g / (1 + exp(-g)) * u.  exp by v_exp_f32 (2^x): the rounding of the
-  // exponent costs |g| * 2^-24 relative to exp(-g), which matters only where
-  // exp(-g) is large, that is where the value is near zero; v_rcp_f32 is
-  // within one unit in the last place.  exp(-g) = inf gives g * 0.
+  // g / (1 + exp(-g)) * u.  exp(-g) = 2^(hi + lo), hi = -g*log2(e) rounded and lo
+  // its rounding error: v_exp_f32 of hi (within one unit), times 1 + lo*ln 2.
+  // The quotient is v_rcp_f32's with one correction.  So the value's error does
+  // not grow with |g| (a rounded exponent alone costs |g| half units, which
+  // moves codes near a tie).  exp(-g) = inf gives g * 0.
   template <int E>
   __device__ __forceinline__ void values(const Row&, uint32_t, uint32_t, const Raw& v,
                                          float (&u)[8], float&) const {
@@ -266,8 +267,15 @@ struct Silu {
     widen<D>(v.u, u);
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-      const float e = __builtin_amdgcn_exp2f(g[i] * -1.44269504088896341f);
-      u[i] = g[i] * __builtin_amdgcn_rcpf(1.0f + e) * u[i];
+      constexpr float kL = -1.44269504088896341f;             // -log2(e), rounded
+      constexpr float kRest = (float)(-1.44269504088896340736 - (double)kL);
+      const float hi = g[i] * kL;
+      const float lo = __builtin_fmaf(g[i], kRest, __builtin_fmaf(g[i], kL, -hi));
+      const float e0 = __builtin_amdgcn_exp2f(hi);
+      const float e = __builtin_fmaf(e0, lo * 0.693147180559945309f, e0);
+      const float t = 1.0f + e, r = __builtin_amdgcn_rcpf(t), q = g[i] * r;
+      const float better = __builtin_fmaf(__builtin_fmaf(-t, q, g[i]), r, q);
+      u[i] = (t < __builtin_inff() ? better : q) * u[i];
     }
   }
   template <int E>
@@ -338,18 +346,34 @@ __device__ __forceinline__ void clear(Joined& lds) {
   if (t >= waves && t < 16) lds.ss[t] = lds.a[t] = 0.0f;
 }
 
-// 8 codes; f = 0 marks a row without codes
-__device__ __forceinline__ u32x2 code8(const float (&u)[8], float f) {
+// 8 codes: round-half-even(127 * u / a) as u*f + 1.5*2^23, one rounding, f = 127/a
+// rounded.  f's rounding moves u*f by at most 127 * 2^-24, so a value within 2^-17
+// of a tie (one in 65000) is rounded from the quotient in 64 bits: that is
+// off by less than 2^-44, and the exact one is a tie or at least 2^-33 away from
+// one (u and a have 24 bits each), so rounded to multiples of 2^-36 it is a tie
+// where the exact one is.  f = 0 marks a row without codes.
+__device__ __forceinline__ u32x2 code8(const float (&u)[8], float f, float a) {
   u32x2 w = {0u, 0u};
   if (f != 0.0f) {
+    constexpr float kMagic = 0x1.8p23f, kNear = 0.5f - 0x1p-17f;
+    float m[8], far = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      m[i] = __builtin_fmaf(u[i], f, kMagic);
+      far = max_abs(far, __builtin_fmaf(u[i], f, -(m[i] - kMagic)));
+    }
+    if (far > kNear) {
+      constexpr double kGrid = 0x1.8p16;
+      const double exact_f = 127.0 / (double)a;
+#pragma unroll
+      for (int i = 0; i < 8; i++)
+        m[i] = (float)__builtin_rint((double)u[i] * exact_f + kGrid - kGrid) + kMagic;
+    }
 #pragma unroll
     for (int k = 0; k < 2; k++) {
-      uint32_t b;
-      rint_byte<0>(b, u[4 * k] * f);
-      rint_byte<1>(b, u[4 * k + 1] * f);
-      rint_byte<2>(b, u[4 * k + 2] * f);
-      rint_byte<3>(b, u[4 * k + 3] * f);
-      w[k] = b;
+      const auto bits = [&](int i) { return __builtin_bit_cast(uint32_t, m[4 * k + i]); };
+      w[k] = __builtin_amdgcn_perm(bits(1), bits(0), 0x0c0c0400u) |
+             __builtin_amdgcn_perm(bits(3), bits(2), 0x04000c0cu);
     }
   }
   return w;
@@ -420,7 +444,7 @@ __global__ __launch_bounds__(Wave ? 64 * kRowsOfAGroup : 1024) void k_rows(Op op
 #pragma unroll
     for (int j = 0; j < V; j++) {
       const uint32_t i0 = 8 * (t + T * j);
-      if (i0 < o.d) store_codes<E>(q + i0, code8(u[j], f), o.d - i0 < 8 ? o.d - i0 : 8);
+      if (i0 < o.d) store_codes<E>(q + i0, code8(u[j], f, a), o.d - i0 < 8 ? o.d - i0 : 8);
     }
     if (t == 0) o.scales[m] = scale;
     if (!Wave && m + gridDim.x < o.M) __syncthreads();         // lds is used again
@@ -455,7 +479,7 @@ __global__ __launch_bounds__(T) void k_rows_long(Op op, RowsOut o) {
       const uint32_t n = o.d - 8 * vec < 8 ? o.d - 8 * vec : 8;
       float u[8];
       op.template again<kAny>(row, vec, n, u);
-      store_codes<kAny>(q + 8 * vec, code8(u, f), n);
+      store_codes<kAny>(q + 8 * vec, code8(u, f, a), n);
     }
     if (threadIdx.x == 0) o.scales[m] = scale;
     if (m + gridDim.x < o.M) __syncthreads();

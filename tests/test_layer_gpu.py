@@ -5,8 +5,10 @@ Tolerances, derived from the operations and fixed before the first run
 (e = 2^-24, half a unit in the last place of binary32):
   h       one binary32 addition and one rounding to 16 bits, as numpy and
           torch do them: bit-exact;
-  codes   of the norm: u = h*weight is exact, a = max|u| is exact, f = 127/a
-          and u*f are single operations: bit-exact;
+  codes   of the norm: u = h*weight is exact, a = max|u| is exact, and the
+          code is the exact quotient's: bit-exact.  In 64 bits 127*u is exact
+          and the quotient rounded once; a tie stays one, and anything else
+          is at least 2^-33 away from one (u and a have 24 bits);
   scale   of the norm: the sum of squares is a chain of at most CHAIN
           additions of positive terms (each within e), so r is within
           (CHAIN/2 + 4) e, and a*r/127 adds two roundings;
@@ -74,8 +76,7 @@ def check_codes(q, s, u, r, tol_scale, label):
         if a < TINY:
             assert s[m] == 0 and not q[m].any(), (label, m, "zero row")
             continue
-        f = np.float32(127) / a
-        want = np.rint(u[m].astype(np.float32) * f)
+        want = np.rint(127.0 * u[m] / np.float64(a))
         assert np.array_equal(q[m], want.astype(np.int8)), (label, m, np.nonzero(q[m] != want))
         exact = float(a) * r[m] / 127
         assert abs(s[m] - exact) <= tol_scale * exact, (label, m, s[m], exact)
