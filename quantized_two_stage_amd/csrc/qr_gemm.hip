@@ -15,9 +15,9 @@
 //            stages run side by side;
 //   k_tile   many tiles: the waves share one tile and one ring; the matrix
 //            units and the loads bound it.
-// Measured (cold weights, bf16): 1 token over 8192x8192 weights 13.1 us, 5.1
-// TB/s of weights where a large copy reaches 5.2; 48 tokens, 8192x4096: 11.9
-// us; 8192^3: 435 us, 2530 TOPS (a library product of the same codes without
+// Measured (cold weights, bf16): 1 token over 8192x8192 weights 12.1 us, 5.5
+// TB/s of weights where a large copy reaches 5.2; 48 tokens, 8192x4096: 11.5
+// us; 8192^3: 428 us, 2570 TOPS (a library product of the same codes without
 // scales: 528 us).
 #include <type_traits>
 
@@ -345,6 +345,14 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_tile(GemmArgs g, Grid gr) {
 // A block of BM tokens by BN channels to a workgroup, whose W waves share the
 // sum: wave w takes stages w, w + W, ... through a ring of S stages of its own
 // in LDS, so the waves wait for nothing but their own loads until the end.
+// Neighbouring tiles start kApart stages apart: all at once they would ask for
+// the same lines of a, and for lines of b a power of two apart, which few of the
+// caches' and the memory's channels hold.  Cold weights, 16384x4096, us: one
+// token 12.2, started together 13.5; 16 tokens 14.0 and 15.7; 48 tokens 15.9 and
+// 17.3.  7, 9 or 13 stages apart come out within 4% of 2 there; at 8192x8192,
+// one token: 12.1 with 2, 12.4 with 7, 13.2 together.
+constexpr uint32_t kApart = 2;
+
 template <int BM, int BN, int W, int S, int D, bool Once>
 __global__ __launch_bounds__(64 * W) void k_split(GemmArgs g, Grid gr) {
   constexpr int FM = (BM + 15) / 16, FN = BN / 16;
@@ -380,8 +388,12 @@ __global__ __launch_bounds__(64 * W) void k_split(GemmArgs g, Grid gr) {
   i32x4 ra = buffer_at(pa), rb = buffer_at(pb);
   // stage s into slot `to`; past the last stage from an empty buffer, from
   // which nothing is fetched
+  const uint32_t rest = steps > 1 ? steps - 1 : 1;        // the last one stays last
+  const uint32_t turn = (uint32_t)__builtin_amdgcn_readfirstlane((int)(tn * kApart % rest));
   const auto load = [&](uint32_t s, uint32_t to) {
-    const uint32_t k = s < steps ? s * kStep : 0u;
+    uint32_t at = s + turn < rest ? s + turn : s + turn - rest;
+    if (s + 1 >= steps) at = s < steps ? s : 0;
+    const uint32_t k = at * kStep;
     end_buffer(ra, s, steps);
     end_buffer(rb, s, steps);
     if (s + 1 == steps && cut_last) offsets(k);
@@ -450,8 +462,9 @@ __global__ __launch_bounds__(64 * W) void k_split(GemmArgs g, Grid gr) {
 // Weights that one row of tiles covers are read by one workgroup only, and a
 // model's weights do not stay in the 256 MB cache until they are used again:
 // past the caches, one token over cold 8192x8192 weights takes 13.1 us instead
-// of 15.4, 8192x4096 8.3 instead of 9.5, 48 tokens 11.9 instead of 12.6.  Where
-// the same 67 MB are read again and again it costs 12.3 against 11.5.
+// of 15.4, 8192x4096 8.3 instead of 9.5, 48 tokens 11.9 instead of 12.6 (before
+// the tiles' starts were set apart, k_split).  Where the same 67 MB are read
+// again and again it costs 12.3 against 11.5.
 template <int BM, int BN, int WM, int WN, int S>
 hipError_t tiles(int dtype, const GemmArgs& g, uint32_t group, hipStream_t st) {
   const Grid gr{(g.M + BM - 1) / BM, (g.N + BN - 1) / BN, group};
@@ -484,10 +497,12 @@ hipError_t split(int dtype, const GemmArgs& g, uint32_t group, hipStream_t st) {
 // launch takes the one whose rounds of 256 workgroups are estimated to end
 // first.  Measured at 1024 tokens x 1024 channels, K = 8192 (64 stages), us:
 // 32x32 of k_split 32 (four rounds), 64x64 of k_split 20.6, 64x64 of k_tile
-// 22.1, 128x128 38, 256x256 98; at 2048 x 16384, K = 4096: 126, 130 and more
+// 22.1, 128x64 28, 128x128 38, 256x256 98; at 2048 x 16384, K = 4096: 126, 130 and more
 // for the first three, 128x128 190, 128x256 139, 256x256 132.  Against the
-// fastest of 40 tilings at each of 73 sizes the rule loses 3% at the median and
-// 22% (half a microsecond, 64x64x16) at most.
+// fastest of 40 tilings at each of 73 sizes, timed before the weights were
+// loaded past the caches, the rule and its kernels are equal at the median and
+// 9.3 us against 6.7 at worst (one token, 300x16384: few workgroups, and the
+// weights of that table lay in the cache).
 struct Variant {
   uint32_t bm, bn, fixed, stage;
   hipError_t (*launch)(int, const GemmArgs&, uint32_t, hipStream_t);
@@ -500,10 +515,11 @@ constexpr Variant kVariants[] = {
     {64, 32, 4000, 190, split<64, 32, 4, 3>, 16},
     {64, 64, 4500, 240, split<64, 64, 4, 2>, 16},
     {64, 64, 3000, 290, tiles<64, 64, 2, 2, 4>, 8},
+    {64, 128, 3400, 360, tiles<64, 128, 2, 4, 5>, 8},
     {128, 64, 3400, 380, tiles<128, 64, 4, 2, 5>, 8},
     {128, 128, 4000, 520, tiles<128, 128, 2, 4, 4>, 8},
     {128, 256, 4500, 780, tiles<128, 256, 2, 4, 3>, 8},
-    {256, 256, 5500, 1400, tiles<256, 256, 2, 4, 2>, 4},
+    {256, 256, 5500, 1350, tiles<256, 256, 4, 2, 2>, 4},
 };
 
 }  // namespace
@@ -516,8 +532,9 @@ hipError_t launch_gemm(int dtype, const GemmArgs& g, hipStream_t st) {
   const Variant* best = nullptr;
   uint64_t least = ~0ull;
   for (const Variant& v : kVariants) {
-    const uint64_t blocks = (uint64_t)((g.M + v.bm - 1) / v.bm) * ((g.N + v.bn - 1) / v.bn);
-    const uint64_t ns = (blocks + 255) / 256 * (v.fixed + steps * v.stage);
+    const uint64_t tm = (g.M + v.bm - 1) / v.bm, blocks = tm * ((g.N + v.bn - 1) / v.bn);
+    uint64_t ns = (blocks + 255) / 256 * (v.fixed + steps * v.stage);
+    if (tm == 1) ns -= ns / 10;              // the weights are read once
     if (ns < least) {
       least = ns;
       best = &v;

@@ -19,9 +19,10 @@ SIZES = {
     "64x64 of k_split": [(333, 2001, 33), (1001, 777, 40), (1001, 1013, 64)],
     "64x64 of k_tile": [(33, 4156, 1), (33, 4103, 2), (34, 4148, 3), (33, 4189, 4), (33, 4426, 5), (4177, 33, 6),
                         (4149, 34, 8)],
-    "128x64": [(133, 5709, 1), (142, 5465, 2), (133, 5720, 4), (129, 5542, 5), (129, 5697, 6), (145, 5463, 7)],
-    "128x128": [(273, 5511, 1), (262, 5681, 3), (258, 5798, 4), (258, 5896, 5), (262, 5971, 6)],
+    "64x128 or 128x64": [(120, 9000, 1), (97, 9011, 4), (120, 9001, 5), (99, 9000, 6), (133, 5709, 1), (142, 5465, 2), (133, 5720, 4), (129, 5542, 5), (129, 5697, 6), (145, 5463, 7)],
+    "64x128": [(273, 5511, 1), (262, 5681, 3), (258, 5798, 4), (258, 5896, 5), (262, 5971, 6)],
     "128x256": [(647, 5468, 1), (654, 5487, 2), (513, 6803, 3), (516, 6967, 4), (667, 5615, 6)],
+    "128x128 of 3 rows of tiles": [(333, 8033, s) for s in (1, 3, 4, 5, 8, 9)],
     "256x256": [(4667, 1537, 1), (4869, 1542, 2), (1161, 6451, 3), (1290, 5895, 4)],
 }
 
