@@ -497,8 +497,8 @@ hipError_t split(int dtype, const GemmArgs& g, uint32_t group, hipStream_t st) {
 // launch takes the one whose rounds of 256 workgroups are estimated to end
 // first.  Measured at 1024 tokens x 1024 channels, K = 8192 (64 stages), us:
 // 32x32 of k_split 32 (four rounds), 64x64 of k_split 20.6, 64x64 of k_tile
-// 22.1, 128x64 28, 128x128 38, 256x256 98; at 2048 x 16384, K = 4096: 126, 130 and more
-// for the first three, 128x128 190, 128x256 139, 256x256 132.  Against the
+// 22.1, 128x64 28, 128x128 38, 256x256 98; at 2048 x 16384, K = 4096: 64x64 of
+// k_tile 251, 128x64 243, 128x128 190, 128x256 139, 256x256 132. Against the
 // fastest of 40 tilings at each of 73 sizes, timed before the weights were
 // loaded past the caches, the rule and its kernels are equal at the median and
 // 9.3 us against 6.7 at worst (one token, 300x16384: few workgroups, and the

@@ -11,11 +11,11 @@
 // u_i*r*127/(a*r) = u_i*127/a, so the codes need the maximum a of u = h*weight
 // alone, and r enters the scale only.
 //
-// HBM bounds long batches: 8192 rows of 8192 (norm, bf16) take 89 us, 5.3 TB/s
-// (a large copy reaches 5.2); 4096 rows of 8192 from 4-bit wire codes 41 us,
-// 4.6 TB/s; the activation of 8192 rows of 4096 30 us, 5.5 TB/s.  Single rows
-// are bound by the latency of a launch, of one read and of the reduction:
-// 3.4 us at 8192 values.
+// HBM bounds long batches: 8192 rows of 8192 (norm, bf16) take 84 to 96 us, 4.9
+// to 5.6 TB/s (a large copy reaches 5.2); 4096 rows of 8192 from asymmetric
+// 4-bit wire codes 41 to 45 us, 4.2 to 4.6 TB/s; the activation of 8192 rows of
+// 4096 31 us, 5.3 TB/s.  Single rows are bound by the latency of a launch, of
+// one read and of the reduction: 3.6 us at 8192 values.
 #include <type_traits>
 
 #include "qr.h"
@@ -505,11 +505,12 @@ hipError_t rows_twice(const Op& op, const RowsOut& o, hipStream_t st) {
 // One vector to a lane wherever a workgroup has the lanes, and no more waves
 // than the row needs: the loads of a row are all on their way at once, few
 // registers are held, and many waves share a CU.  The norm from 16-bit rows,
-// us: 8192 rows of 8192 with 1024 lanes x 1 vector 89, 512 x 2 88, 256 x 4 98,
-// 128 x 8 117; of 4096 with 512 x 1 45, 256 x 2 48, 1024 x 1 56; one row of 8192
-// 3.4, 3.4, 4.2, 5.9; 1024 rows of 5003 with 640 lanes 14.4, with 1024 lanes
-// 19.9.  Rows that are whole vectors apart from the others: the former with
-// the latter's loads take 113 instead of 98 (256 x 4).
+// us, when this was chosen: 8192 rows of 8192 with 1024 lanes x 1 vector 89,
+// 512 x 2 88, 256 x 4 98, 128 x 8 117; of 4096 with 512 x 1 45, 256 x 2 48,
+// 1024 x 1 56; one row of 8192 3.4, 3.4, 4.2, 5.9; 1024 rows of 5003 with 640
+// lanes 14.4, with 1024 lanes 19.9 (exact codes have added 0.3 to 3 us since).
+// Rows that are whole vectors apart from the others: the former with the
+// latter's loads take 113 instead of 98 (256 x 4).
 template <class Op, int E>
 hipError_t rows_by_length(const Op& op, const RowsOut& o, hipStream_t st) {
   if (o.d <= 512) return rows_in_registers<Op, true, 1, E>(op, o, st);
