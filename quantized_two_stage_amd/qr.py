@@ -286,6 +286,11 @@ def _mat(what, t, rows, cols, dtype, dev):
     if t.dtype is not dtype or t.get_device() != dev or t.shape != (rows, cols):
         _refuse(what, t, dtype, dev,
                 "%s has shape %s: %s expected" % (what, tuple(t.shape), (rows, cols)))
+    return _ld(what, t, rows, cols)
+
+
+def _ld(what, t, rows, cols):
+    """The row stride of a matrix whose shape, type and device are known."""
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError("%s: the values of a row are not contiguous" % what)
@@ -351,7 +356,7 @@ def qr_add_rmsnorm_q8(x, residual, weight, eps, h, q, scales, stream=None):
     M, d = _matrix_shape("x", x)
     code = _type16(x, "x")
     dev = _device(x, "x")
-    ldx = _mat("x", x, M, d, x.dtype, dev)
+    ldx = _ld("x", x, M, d)
     pr, ldr, pw, ph, ldh, pq, ldq, ps = _norm_args(residual, weight, h, q, scales, M, d, x.dtype,
                                                    dev)
     _check(LIB.qr_add_rmsnorm_q8(code, x.data_ptr(), ldx, pr, ldr, pw, eps, M, d, ph, ldh, pq,
@@ -390,7 +395,7 @@ def qr_silu_mul_q8(gu, q, scales, stream=None):
     d = d2 // 2
     code = _type16(gu, "gu")
     dev = _device(gu, "gu")
-    _check(LIB.qr_silu_mul_q8(code, gu.data_ptr(), _mat("gu", gu, M, d2, gu.dtype, dev), M, d,
+    _check(LIB.qr_silu_mul_q8(code, gu.data_ptr(), _ld("gu", gu, M, d2), M, d,
                               q.data_ptr(), _mat("q", q, M, d, torch.int8, dev),
                               _vec("scales", scales, M, torch.float32, dev),
                               _stream_on(dev, stream)))
