@@ -527,6 +527,11 @@ constexpr Variant kVariants[] = {
 hipError_t launch_gemm(int dtype, const GemmArgs& g, hipStream_t st) {
   // up to 8 tokens only 8 rows of a are staged: 1 token, 2048x8192 7.1 us
   // against 8.8 (16x32) with 16 rows; 16384x1024 6.4 against 6.6
+  // Eight waves where a CU has one workgroup at most and the sum is long: 1
+  // token, 300x16384 8.1 against 9.3 with four, 2048x8192 6.0 and 6.7; elsewhere
+  // four: 16384x4096 12.1 against 14.1, 1000x1000 3.2 and 3.3.
+  if (g.M <= 8 && g.N <= 16 * 256 && g.K >= 32 * kStep)
+    return split<8, 16, 8, 2>(dtype, g, 1, st);
   if (g.M <= 8) return split<8, 16, 4, 3>(dtype, g, 1, st);
   const uint64_t steps = (g.K + kStep - 1) / kStep;
   const Variant* best = nullptr;

@@ -10,7 +10,8 @@ pytestmark = pytest.mark.gpu
 
 # tokens, channels, stages; the tile each list is for
 SIZES = {
-    "8x16": [(1, 33, s) for s in (1, 2, 4, 5, 8, 11, 12, 13, 24, 25)] + [(8, 50, 7), (5, 17, 128)],
+    "8x16": [(1, 33, s) for s in (1, 2, 4, 5, 8, 11, 12, 13, 24, 25)] + [(8, 50, 7), (5, 17, 128), (3, 4097, 33), (2, 4500, 40)],
+    "8x16 of 8 waves": [(1, 33, s) for s in (33, 34, 39, 40, 41, 47, 48, 49, 64)] + [(8, 4095, 33), (7, 100, 129)],
     "16x16": [(9, 4, s) for s in (1, 2, 7, 8, 9, 15, 16, 17, 23, 24, 25)] + [(27, 35, 128)],
     "16x32": [(2050, 17, 1), (2121, 17, 2), (2071, 17, 3), (2055, 17, 4), (2049, 17, 5), (2116, 17, 12),
               (2095, 17, 13)],
