@@ -37,6 +37,7 @@ constexpr uint32_t kStep = 128;       // codes of the sum in one stage of the ti
 // assembly since the compiler, where it cannot tell two LDS buffers apart,
 // would wait for the load before any LDS read: the caller waits.  It has no
 // output register, so nothing is written behind the compiler's back but LDS.
+// m0 is a reserved register, in which the compiler keeps nothing.
 // Once: past the caches, for what no other workgroup reads.
 template <bool Once>
 __device__ __forceinline__ void load_to_lds(i32x4 rsrc, uint32_t lds, uint32_t voff,
