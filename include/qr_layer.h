@@ -83,9 +83,11 @@ int qr_gather_add_rmsnorm_q8(qr_codec codec, qr_dtype dtype, const void* wire,
                              float eps, size_t M, size_t d, void* h, size_t ldh, int8_t* q,
                              size_t ldq, float* scales, void* stream);
 
-/* Codes and scales of v_i = g_i / (1 + exp(-g_i)) * u_i in binary32, where
- * row m of gu (row stride ldg >= 2d) holds the d gate values g and then the d
- * up values u.  d in 1..QR_MAX_ROW. */
+/* Codes and scales of v_i = g_i / (1 + exp(-g_i)) * u_i, where row m of gu (row
+ * stride ldg >= 2d) holds the d gate values g and then the d up values u.  v is
+ * held in binary32, within 16 * 2^-24 of its value for every finite g and u
+ * (gates where exp(-g) passes the largest binary32 among them); a v that itself
+ * passes it counts as an infinity.  d in 1..QR_MAX_ROW. */
 int qr_silu_mul_q8(qr_dtype dtype, const void* gu, size_t ldg, size_t M, size_t d, int8_t* q,
                    size_t ldq, float* scales, void* stream);
 
