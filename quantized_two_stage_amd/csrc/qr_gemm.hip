@@ -36,24 +36,23 @@ constexpr uint32_t kStep = 128;       // codes of the sum in one stage of the ti
 // the wave, without passing through registers; s_waitcnt vmcnt covers it.  In
 // assembly since the compiler, where it cannot tell two LDS buffers apart,
 // would wait for the load before any LDS read: the caller waits.  It has no
-// output register, so nothing is written behind the compiler's back but LDS.
-// m0 is a reserved register, in which the compiler keeps nothing.
+// output register, so nothing is written behind the compiler's back but LDS:
+// m0, which holds the LDS address, is an input that the compiler sets (the wait
+// state is the one that a load through m0 needs after that).
 // Once: past the caches, for what no other workgroup reads.
 template <bool Once>
 __device__ __forceinline__ void load_to_lds(i32x4 rsrc, uint32_t lds, uint32_t voff,
                                             uint32_t soff) {
   if constexpr (Once)
-    asm volatile(
-        "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
-        :
-        : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
-        : "memory");
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+                 :
+                 : "{m0}"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+                 : "memory");
   else
-    asm volatile(
-        "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-        :
-        : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
-        : "memory");
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "{m0}"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+                 : "memory");
 }
 // A buffer that starts at p, for load_to_lds.  The wait states are those that
 // a memory instruction needs after a vector instruction (readfirstlane) wrote
