@@ -20,17 +20,17 @@
 // us; 8192^3: 428 us, 2570 TOPS (a library product of the same codes without
 // scales: 528 us).
 #include <type_traits>
+#include <utility>
 
 #include "qr.h"
 #include "qr_device.h"
+#include "qr_gemm_tiles.h"
 #include "qr_layer_internal.h"
 
 namespace qr {
 namespace {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
-
-constexpr uint32_t kStep = 128;       // codes of the sum in one stage of the tile kernel
 
 // 16 bytes from base + voff + soff to LDS byte lds + 16*lane, for every lane of
 // the wave, without passing through registers; s_waitcnt vmcnt covers it.  In
@@ -465,87 +465,38 @@ __global__ __launch_bounds__(64 * W) void k_split(GemmArgs g, Grid gr) {
 // of 15.4, 8192x4096 8.3 instead of 9.5, 48 tokens 11.9 instead of 12.6 (before
 // the tiles' starts were set apart, k_split).  Where the same 67 MB are read
 // again and again it costs 12.3 against 11.5.
-template <int BM, int BN, int WM, int WN, int S>
-hipError_t tiles(int dtype, const GemmArgs& g, uint32_t group, hipStream_t st) {
-  const Grid gr{(g.M + BM - 1) / BM, (g.N + BN - 1) / BN, group};
-  const dim3 grid(gr.tm * gr.tn), block(64 * WM * WN);
-  const auto kernel = [&](auto d) {
+template <int I>
+hipError_t launch_tile(int dtype, const GemmArgs& g, hipStream_t st) {
+  constexpr Tile t = kTiles[I];
+  const Grid gr{tile_rows(t, g.M), (g.N + t.bn - 1) / t.bn, t.group};
+  const dim3 grid(gr.tm * gr.tn), block(64 * t.wm * (t.wn ? t.wn : 1));
+  const auto kernel = [&](auto d, auto once) {
     constexpr int D = decltype(d)::value;
-    if (gr.tm == 1) k_tile<BM, BN, WM, WN, S, D, true><<<grid, block, 0, st>>>(g, gr);
-    else k_tile<BM, BN, WM, WN, S, D, false><<<grid, block, 0, st>>>(g, gr);
+    constexpr bool Once = decltype(once)::value;
+    if constexpr (t.wn == 0) k_split<t.bm, t.bn, t.wm, t.stages, D, Once><<<grid, block, 0, st>>>(g, gr);
+    else k_tile<t.bm, t.bn, t.wm, t.wn, t.stages, D, Once><<<grid, block, 0, st>>>(g, gr);
   };
-  if (dtype == kF16) kernel(std::integral_constant<int, kF16>{});
-  else kernel(std::integral_constant<int, kBF16>{});
-  return hipGetLastError();
-}
-template <int BM, int BN, int W, int S>
-hipError_t split(int dtype, const GemmArgs& g, uint32_t group, hipStream_t st) {
-  const Grid gr{(g.M + BM - 1) / BM, (g.N + BN - 1) / BN, group};
-  const dim3 grid(gr.tm * gr.tn), block(64 * W);
-  const auto kernel = [&](auto d) {
-    constexpr int D = decltype(d)::value;
-    if (gr.tm == 1) k_split<BM, BN, W, S, D, true><<<grid, block, 0, st>>>(g, gr);
-    else k_split<BM, BN, W, S, D, false><<<grid, block, 0, st>>>(g, gr);
+  const auto of_type = [&](auto d) {
+    if (gr.tm == 1) kernel(d, std::true_type{});
+    else kernel(d, std::false_type{});
   };
-  if (dtype == kF16) kernel(std::integral_constant<int, kF16>{});
-  else kernel(std::integral_constant<int, kBF16>{});
+  if (dtype == kF16) of_type(std::integral_constant<int, kF16>{});
+  else of_type(std::integral_constant<int, kBF16>{});
   return hipGetLastError();
 }
 
-// Tiles and what a workgroup of each was measured to take where every CU has
-// one at most: ns to start and end, and ns for each 128 codes of the sum.  The
-// launch takes the one whose rounds of 256 workgroups are estimated to end
-// first.  Measured at 1024 tokens x 1024 channels, K = 8192 (64 stages), us:
-// 32x32 of k_split 32 (four rounds), 64x64 of k_split 20.6, 64x64 of k_tile
-// 22.1, 128x64 28, 128x128 38, 256x256 98; at 2048 x 16384, K = 4096: 64x64 of
-// k_tile 251, 128x64 243, 128x128 190, 128x256 139, 256x256 132. Against the
-// fastest of 40 tilings at each of 73 sizes, timed before the weights were
-// loaded past the caches, the rule and its kernels are equal at the median and
-// 9.3 us against 6.7 at worst (one token, 300x16384: few workgroups, and the
-// weights of that table lay in the cache).
-struct Variant {
-  uint32_t bm, bn, fixed, stage;
-  hipError_t (*launch)(int, const GemmArgs&, uint32_t, hipStream_t);
-  uint32_t group;
-};
-constexpr Variant kVariants[] = {
-    {16, 16, 2800, 65, split<16, 16, 8, 2>, 16},
-    {16, 32, 2900, 100, split<16, 32, 4, 3>, 16},
-    {32, 32, 3100, 130, split<32, 32, 4, 2>, 16},
-    {64, 32, 4000, 190, split<64, 32, 4, 3>, 16},
-    {64, 64, 4500, 240, split<64, 64, 4, 2>, 16},
-    {64, 64, 3000, 290, tiles<64, 64, 2, 2, 4>, 8},
-    {64, 128, 3400, 360, tiles<64, 128, 2, 4, 5>, 8},
-    {128, 64, 3400, 380, tiles<128, 64, 4, 2, 5>, 8},
-    {128, 128, 4000, 520, tiles<128, 128, 2, 4, 4>, 8},
-    {128, 256, 4500, 780, tiles<128, 256, 2, 4, 3>, 8},
-    {256, 256, 5500, 1350, tiles<256, 256, 4, 2, 2>, 4},
-};
+using Launch = hipError_t (*)(int, const GemmArgs&, hipStream_t);
+template <int... I>
+Launch launch_of(int tile, std::integer_sequence<int, I...>) {
+  static constexpr Launch table[] = {launch_tile<I>...};
+  return table[tile];
+}
 
 }  // namespace
 
 hipError_t launch_gemm(int dtype, const GemmArgs& g, hipStream_t st) {
-  // up to 8 tokens only 8 rows of a are staged: 1 token, 2048x8192 7.1 us
-  // against 8.8 (16x32) with 16 rows; 16384x1024 6.4 against 6.6
-  // Eight waves where a CU has one workgroup at most and the sum is long: 1
-  // token, 300x16384 8.1 against 9.3 with four, 2048x8192 6.0 and 6.7; elsewhere
-  // four: 16384x4096 12.1 against 14.1, 1000x1000 3.2 and 3.3.
-  if (g.M <= 8 && g.N <= 16 * 256 && g.K >= 32 * kStep)
-    return split<8, 16, 8, 2>(dtype, g, 1, st);
-  if (g.M <= 8) return split<8, 16, 4, 3>(dtype, g, 1, st);
-  const uint64_t steps = (g.K + kStep - 1) / kStep;
-  const Variant* best = nullptr;
-  uint64_t least = ~0ull;
-  for (const Variant& v : kVariants) {
-    const uint64_t tm = (g.M + v.bm - 1) / v.bm, blocks = tm * ((g.N + v.bn - 1) / v.bn);
-    uint64_t ns = (blocks + 255) / 256 * (v.fixed + steps * v.stage);
-    if (tm == 1) ns -= ns / 10;              // the weights are read once
-    if (ns < least) {
-      least = ns;
-      best = &v;
-    }
-  }
-  return best->launch(dtype, g, best->group, st);
+  return launch_of(choose_tile(g.M, g.N, g.K),
+                   std::make_integer_sequence<int, kTileCount>{})(dtype, g, st);
 }
 
 }  // namespace qr
