@@ -477,7 +477,8 @@ hipError_t launch_tile(int dtype, const GemmArgs& g, hipStream_t st) {
     else k_tile<t.bm, t.bn, t.wm, t.wn, t.stages, D, Once><<<grid, block, 0, st>>>(g, gr);
   };
   const auto of_type = [&](auto d) {
-    if (gr.tm == 1) kernel(d, std::true_type{});
+    if constexpr (t.bm <= 8) kernel(d, std::true_type{});    // never more tokens
+    else if (gr.tm == 1) kernel(d, std::true_type{});
     else kernel(d, std::false_type{});
   };
   if (dtype == kF16) of_type(std::integral_constant<int, kF16>{});

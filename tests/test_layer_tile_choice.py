@@ -70,3 +70,10 @@ def test_every_kernel_that_a_size_takes_is_run(choose):
     missing = {tile: size for tile, size in taken.items() if tile not in run}
     assert not missing, missing
     assert len(taken) == 24, sorted(taken)         # 11 tiles of either kind, and two of up to 8 tokens
+
+
+def test_tiles_of_8_tokens_are_one_row(choose):
+    """the launch has these two only as kernels of one row of tiles"""
+    sizes = [(M, N, K) for M in range(1, 70) for N in (1, 300, 4096, 4097, 1 << 20) for K in (1, 4095, 4096, 131071)]
+    for size, got in zip(sizes, choose(sizes)):
+        assert (got[0] == 8) == (size[0] <= 8) and (got[0] != 8 or got[4] == "one"), size
