@@ -58,7 +58,6 @@ class FeedForward:
         self.q, self.s = qr.alloc_q8(M, d, device)
         self.gu = torch.empty(M, 2 * f, dtype=dtype, device=device)
         self.act, self.act_s = qr.alloc_q8(M, f, device)
-        self.spaces = [qr.alloc_gemm_workspace(M, 2 * f, d), qr.alloc_gemm_workspace(M, d, f)]
 
     def _reduce_and_norm(self, weight):
         qr.qr_quantize_recv(self.codec, list(self.summands), self.recv)
@@ -71,9 +70,9 @@ class FeedForward:
         for weight, first, second in self.layers:
             self._reduce_and_norm(weight)
             for r in range(self.W):                       # on a node: every rank its own
-                qr.qr_gemm_i8(self.q, self.s, *first[r], self.gu, workspace=self.spaces[0])
+                qr.qr_gemm_i8(self.q, self.s, *first[r], self.gu)
                 qr.qr_silu_mul_q8(self.gu, self.act, self.act_s)
-                qr.qr_gemm_i8(self.act, self.act_s, *second[r], self.summands[r], workspace=self.spaces[1])
+                qr.qr_gemm_i8(self.act, self.act_s, *second[r], self.summands[r])
         self._reduce_and_norm(self.last)
         return self.h, self.q, self.s
 

@@ -405,8 +405,8 @@ def qr_silu_mul_q8(gu, q, scales, stream=None):
 def qr_gemm_i8(a, sa, b, sb, c, bias=None, workspace=None, stream=None):
     """c = (a @ b^T in 32-bit integers) * sa * sb (+ bias), rounded once to c's
     type.  a: [M, K] int8 codes of the tokens and sa their M float32 scales,
-    b: [N, K] int8 codes of the weights and sb their N scales; workspace:
-    alloc_gemm_workspace(M, N, K)."""
+    b: [N, K] int8 codes of the weights and sb their N scales.  No size needs a
+    workspace; one that is passed is left alone."""
     M, K = _matrix_shape("a", a)
     N = _matrix_shape("b", b)[0]
     code = _type16(c, "c")
