@@ -290,11 +290,12 @@ def _mat(what, t, rows, cols, dtype, dev):
 
 
 def _ld(what, t, rows, cols):
-    """The row stride of a matrix whose shape, type and device are known."""
+    """The row stride of a matrix whose shape, type and device are known (of a
+    single row the shortest there is: its own says nothing)."""
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError("%s: the values of a row are not contiguous" % what)
-    return ld if rows > 1 else max(ld, cols)
+    return ld if rows > 1 else cols
 
 
 def _vec(what, t, n, dtype, dev):
@@ -310,7 +311,7 @@ def _codes(what, t, rows, cols, dev):
     the last one's padding inside the tensor's storage."""
     ld = _mat(what, t, rows, cols, torch.int8, dev)
     if rows == 1:
-        ld = -(-ld // 16) * 16
+        ld = -(-cols // 16) * 16
     if cols % 16 and rows > 0 and (t.storage_offset() + (rows - 1) * ld + -(-cols // 16) * 16
                                    > t.untyped_storage().nbytes()):
         raise ValueError("%s: the padding of its last row up to a multiple of 16 is outside "
