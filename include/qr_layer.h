@@ -34,7 +34,8 @@
  *   - M == 0 is a batch without tokens: the call returns QR_OK and launches
  *     nothing (pointers may be NULL).
  *   - Outputs must not overlap inputs or each other, except where a function
- *     says so.
+ *     says so.  Matrices whose rows lie between one another may share a buffer
+ *     if their strides are the same number of bytes (columns of one buffer).
  */
 #ifndef QR_LAYER_H
 #define QR_LAYER_H

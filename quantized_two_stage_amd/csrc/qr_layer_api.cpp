@@ -44,9 +44,15 @@ int check(const Rows& r) {
   return QR_OK;
 }
 
+// Extents that meet, but for rows of one stride in bytes that lie between one
+// another (columns of one buffer).
 bool overlap(const Rows& a, const Rows& b) {
   const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-  return x < y + b.bytes() && y < x + a.bytes();
+  if (x >= y + b.bytes() || y >= x + a.bytes()) return false;
+  const size_t stride = a.ld * a.elem;
+  if (stride != b.ld * b.elem) return true;
+  const size_t at = y >= x ? (y - x) % stride : stride - 1 - (x - y - 1) % stride;
+  return at < a.cols * a.elem || at + b.cols * b.elem > stride;
 }
 
 int check_apart(const Rows& a, const Rows& b) {
