@@ -57,7 +57,7 @@ extern "C" {
  * after this layer's addition; then codes and scales of
  *     h_i * weight_i * r,   r = 1 / sqrt(mean(h^2) + eps).
  * The codes are those of u_i = h_i * weight_i (exact in binary32), since r
- * is common to the row and cancels in them; scales[m] = a * r / 127.  The
+ * is common to the row and cancels in them; scales[m] = a / 127 * r.  The
  * sum of squares is held in binary32; a row where it overflows counts as
  * holding an infinity.
  *   x         M x d, row stride ldx

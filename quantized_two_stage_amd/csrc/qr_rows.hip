@@ -421,7 +421,7 @@ __device__ __forceinline__ float row_scale(const Op& op, float ss, float a, uint
   const float r = op.factor(ss, d);
   const bool fine = a < kInf && (!Op::kNorm || ss < kInf);    // false for NaN
   const bool use = fine && a >= kTiny;
-  scale = use ? a * r / 127.0f : fine ? 0.0f : __builtin_nanf("");
+  scale = use ? a / 127.0f * r : fine ? 0.0f : __builtin_nanf("");      // a * r may overflow
   return use ? 127.0f / a : 0.0f;
 }
 
