@@ -31,6 +31,8 @@
  *     Rows of 16-bit values may start at any element (2-byte alignment).
  *   - dtype is QR_FP16 or QR_BF16 (qr_gather_add_rmsnorm_q8 also takes
  *     QR_BF16_VIA_FP16) and is the type of every 16-bit buffer of a call.
+ *   - M and N are at most 2^22 and row strides at most 2^40 elements (those of
+ *     qr_gemm_i8's codes less, see there); QR_ERR_SIZE and QR_ERR_ARG above.
  *   - M == 0 is a batch without tokens: the call returns QR_OK and launches
  *     nothing (pointers may be NULL).
  *   - Outputs must not overlap inputs or each other, except where a function

@@ -13,12 +13,15 @@
 //            tile, each with a ring of its own and no barrier; latency bounds
 //            a stage (0.065 us at 16x16, 0.24 us at 64x64), so the sum's
 //            stages run side by side;
-//   k_tile   many tiles: the waves share one tile and one ring; the matrix
-//            units and the loads bound it.
-// Measured (cold weights, bf16): 1 token over 8192x8192 weights 12.1 us, 5.5
-// TB/s of weights where a large copy reaches 5.2; 48 tokens, 8192x4096: 11.5
-// us; 8192^3: 428 us, 2570 TOPS (a library product of the same codes without
-// scales: 528 us).
+//   k_tile   many tiles: the waves share one tile and one ring; the loads to
+//            LDS bound a stage, at 256x256 the matrix units too.
+// A stage of k_tile, ns, with 256 workgroups: 64x128 365, without its matrix
+// instructions 348, without its reads of LDS 373, without its loads 270;
+// 128x128 557, 471, 494, 431; 256x256 1661, 1376, 1748, 1105.
+// Measured (cold weights): 1 token over 8192x8192 weights 12 to 12.6 us, 5.3
+// to 5.6 TB/s (plain reads reach 6.8); 48 tokens, 8192x4096: 11.1 to 13 us;
+// 8192^3: 424 to 442 us, 2490 to 2590 TOPS, the matrix units busy 67% of the
+// time (a library product of the same codes without scales: 528 us).
 #include <type_traits>
 #include <utility>
 
@@ -350,7 +353,9 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_tile(GemmArgs g, Grid gr) {
 // caches' and the memory's channels hold.  Cold weights, 16384x4096, us: one
 // token 12.2, started together 13.5; 16 tokens 14.0 and 15.7; 48 tokens 15.9 and
 // 17.3.  7, 9 or 13 stages apart come out within 4% of 2 there; at 8192x8192,
-// one token: 12.1 with 2, 12.4 with 7, 13.2 together.
+// one token: 12.1 with 2, 12.4 with 7, 13.2 together.  k_tile starts its tiles
+// together: apart, a stage takes 396 ns instead of 365 at 64x128, 597 instead of
+// 557 at 128x128, and 1562 instead of 1661 at 256x256.
 constexpr uint32_t kApart = 2;
 
 template <int BM, int BN, int W, int S, int D, bool Once>

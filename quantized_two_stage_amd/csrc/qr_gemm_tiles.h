@@ -13,14 +13,15 @@ constexpr uint32_t kStep = 128;       // codes of the sum in one stage
 // Tiles and what a workgroup of each was measured to take where every CU has
 // one at most: ns to start and end, and ns for each stage of the sum.  The
 // launch takes the one whose rounds of 256 workgroups are estimated to end
-// first.  Measured at 1024 tokens x 1024 channels, K = 8192 (64 stages), us:
-// 32x32 of k_split 32 (four rounds), 64x64 of k_split 20.6, 64x64 of k_tile
-// 22.1, 128x64 28, 128x128 38, 256x256 98; at 2048 x 16384, K = 4096: 64x64 of
-// k_tile 251, 128x64 243, 128x128 190, 128x256 139, 256x256 132. Against the
-// fastest of 40 tilings at each of 73 sizes, timed before the weights were
-// loaded past the caches, the rule and its kernels are equal at the median and
-// 9.3 us against 6.7 at worst (one token, 300x16384: few workgroups, and the
-// weights of that table lay in the cache).
+// first.  Measured with cold weights at 1024 tokens x 1024 channels, K = 8192
+// (64 stages), us: 16x16 58, 32x32 31 (four rounds), 64x64 of k_split 20.9;
+// at 2048 x 16384, K = 1024: 64x64 of k_tile 97, 64x128 98, 128x64 101, 128x128
+// 75, 128x256 59, 256x256 50.
+// The rule against the fastest of these tiles at each of 158 sizes (10 shapes of
+// weights from 300x16384 to 16384x1024, 1 to 2048 tokens, cold weights): 1.00
+// at the median, within 1.024 at nine of ten, 1.14 at worst (48 tokens, 5003x2050:
+// 9.8 us against 8.6 in 16x32).  The estimate has no term for the weights' bytes:
+// they take as long in every tile of one row of tiles.
 struct Tile {
   uint32_t bm, bn;                    // tokens and channels
   uint32_t wm, wn;                    // waves; wn == 0: wm waves that share the sum (k_split)
@@ -63,7 +64,10 @@ inline int choose_tile(uint32_t M, uint32_t N, uint32_t K) {
     const Tile& t = kTiles[i];
     const uint64_t tm = tile_rows(t, M), blocks = tm * ((N + t.bn - 1) / t.bn);
     uint64_t ns = (blocks + 255) / 256 * (t.start + steps * t.stage);
-    if (tm == 1) ns -= ns / 10;              // the weights are read once
+    // the weights are read once, past the caches: where this decides, 96 tokens
+    // over 11008x4096 take 16.8 us against 18.7 (128x64, 64x128), 128 over
+    // 16384x1024 8.4 against 9.3
+    if (tm == 1) ns -= ns / 10;
     if (ns < least) {
       least = ns;
       best = i;

@@ -11,10 +11,10 @@
 // u_i*r*127/(a*r) = u_i*127/a, so the codes need the maximum a of u = h*weight
 // alone, and r enters the scale only.
 //
-// HBM bounds long batches: 8192 rows of 8192 (norm, bf16) take 84 to 96 us, 4.9
-// to 5.6 TB/s (a large copy reaches 5.2); 4096 rows of 8192 from asymmetric
-// 4-bit wire codes 41 to 45 us, 4.2 to 4.6 TB/s; the activation of 8192 rows of
-// 4096 31 us, 5.3 TB/s.  Single rows are bound by the latency of a launch, of
+// HBM bounds long batches: 8192 rows of 8192 (norm, bf16) take 82 to 96 us, 4.9
+// to 5.7 TB/s (a large copy reaches 5.2); 4096 rows of 8192 from asymmetric
+// 4-bit wire codes 40 to 45 us, 4.2 to 4.7 TB/s (48 under the cast option); the
+// activation of 8192 rows of 4096 31 to 33 us, 5.2 to 5.4 TB/s.  Single rows are bound by the latency of a launch, of
 // one read and of the reduction: 3.6 us at 8192 values.
 #include <type_traits>
 
@@ -534,7 +534,9 @@ hipError_t rows_twice(const Op& op, const RowsOut& o, hipStream_t st) {
 // 1024 x 1 56; one row of 8192 3.4, 3.4, 4.2, 5.9; 1024 rows of 5003 with 640
 // lanes 14.4, with 1024 lanes 19.9 (exact codes have added 0.3 to 3 us since).
 // Rows that are whole vectors apart from the others: the former with the
-// latter's loads take 113 instead of 98 (256 x 4).
+// latter's loads take 113 instead of 98 (256 x 4).  The norm of lengths of 16385
+// to 32767 that are no multiple of 8 needs more than the 128 registers that 1024
+// lanes have, and 12 are spilled: 500 rows of 20003 take 28.6, of 20000 22.1.
 template <class Op, int E>
 hipError_t rows_by_length(const Op& op, const RowsOut& o, hipStream_t st) {
   if (o.d <= 512) return rows_in_registers<Op, true, 1, E>(op, o, st);
