@@ -14,7 +14,7 @@
 // HBM bounds long batches: 8192 rows of 8192 (norm, bf16) take 82 to 96 us, 4.9
 // to 5.7 TB/s (a large copy reaches 5.2); 4096 rows of 8192 from asymmetric
 // 4-bit wire codes 40 to 45 us, 4.2 to 4.7 TB/s (48 under the cast option); the
-// activation of 8192 rows of 4096 31 to 33 us, 5.2 to 5.4 TB/s.  Single rows are bound by the latency of a launch, of
+// activation of 8192 rows of 4096 30 to 32 us, 5.3 to 5.7 TB/s.  Single rows are bound by the latency of a launch, of
 // one read and of the reduction: 3.6 us at 8192 values.
 #include <type_traits>
 
@@ -269,34 +269,38 @@ struct Silu {
   // g / (1 + exp(-g)) * u, as g*e / (1 + e) * u with e = exp(-|g|) where g is
   // negative and with g in place of g*e elsewhere, so that nothing overflows on
   // the way to a small value: within 16 * 2^-24 of the value whatever the gate.
-  // The quotient is v_rcp_f32's with one correction (1 <= 1 + e <= 2).  exp(-|g|)
-  // for |g| <= 80 only, a normal number that no instruction flushes; above,
-  // 1 + e rounds to 1 all the same, and a gate below -80 leaves the rest of its
-  // exponential to u: u * exp(g + 80), in two factors of half the exponent, of
-  // which one that is flushed to 0 stands for a value below any binary32.  An
-  // infinity or NaN in g or u comes out as one (inf * 0 among them).  8192 rows
-  // of 4096, bf16: 31.7 us, and 33.3 where every wave has a gate below -80.
+  // The quotient is v_rcp_f32's with one correction (1 <= 1 + e <= 2).  This is
+  // done for |g| <= 64, where e is a normal number that no instruction flushes.
+  // A gate beyond becomes +-64 and leaves the rest to u: |g|/64 (exact), and
+  // exp(g + 64) if it is negative, in two factors of half the exponent, of
+  // which one that is flushed to 0 stands for a value below any binary32; 1 + e
+  // rounds to 1 all the same.  An infinity or NaN in g or u comes out as one
+  // (inf * 0 among them).  8192 rows of 4096, bf16: 31.4 us, and 32.5 where
+  // every wave has a gate beyond.
   template <int E>
   __device__ __forceinline__ void values(const Row&, uint32_t, uint32_t, const Raw& v,
                                          float (&u)[8], float&) const {
-    constexpr float kFar = 80.0f;
+    constexpr float kFar = 64.0f;
     float g[8];
     widen<D>(v.g, g);
     widen<D>(v.u, u);
-    float least = g[0];
+    float most = 0.0f;
 #pragma unroll
-    for (int i = 1; i < 8; i++) least = __builtin_elementwise_minimum(least, g[i]);
-    if (!(least >= -kFar)) {                                 // rare; a NaN hides no gate
+    for (int i = 0; i < 8; i++) most = max_abs(most, g[i]);
+    if (!(most <= kFar)) {                                   // rare; a NaN hides no gate
 #pragma unroll
       for (int i = 0; i < 8; i++) {
-        const float x = __builtin_elementwise_minimum(-0.5f * (g[i] + kFar), 500.0f);
-        const float half = exp_minus(x);
-        if (g[i] < -kFar) u[i] = u[i] * half * half;
+        const float x = __builtin_fabsf(g[i]);
+        const float half = exp_minus(__builtin_elementwise_minimum(0.5f * (x - kFar), 500.0f));
+        if (x > kFar) {
+          u[i] = (g[i] < 0.0f ? u[i] * half * half : u[i]) * (x / kFar);
+          g[i] = __builtin_copysignf(kFar, g[i]);
+        }
       }
     }
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-      const float e = exp_minus(__builtin_elementwise_minimum(__builtin_fabsf(g[i]), kFar));
+      const float e = exp_minus(__builtin_fabsf(g[i]));
       const float t = 1.0f + e, r = __builtin_amdgcn_rcpf(t);
       const float top = g[i] < 0.0f ? g[i] * e : g[i], q = top * r;
       u[i] *= __builtin_fmaf(__builtin_fmaf(-t, q, top), r, q);

@@ -3,10 +3,10 @@ and rows whose gates are all the same (where the row's scale is as small as the 
 
 Tolerance, derived before the first run (e = 2^-24, half a unit in the last place of binary32): exp(-|g|) is v_exp_f32's
 (one unit, 2e) times a correction (e); the product with g, 1 + exp, the corrected quotient and the product with u are
-within e each: 7e.  Below -80 u is first multiplied twice by the root of exp(g + 80): 2 * (3e + e) more.  So v is within
-15e of its value, whatever the gate, counted as 16e, or within 2^-148 where it is subnormal; the largest magnitude a
-likewise, the scale a/127 within e more, and the code, of the exact quotient of these, within half a step and
-127 * 2 * 16e (and the comparison's own roundings)."""
+within e each: 7e.  Beyond 64 (where 1 + exp is 1 and the quotient exact: 5e) u is first multiplied by |g|/64 (e) and, for
+negative gates, twice by the root of exp(g + 64): 2 * (3e + e) more.  So v is within 14e of its value, whatever the gate,
+counted as 16e, or within 2^-148 where it is subnormal; the largest magnitude a likewise, the scale a/127 within e more,
+and the code, of the exact quotient of these, within half a step and 127 * 2 * 16e (and the comparison's own roundings)."""
 import pytest
 import torch
 
