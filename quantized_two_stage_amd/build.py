@@ -1,5 +1,5 @@
-"""Build libqr.so (the HIP kernels and the C ABI of include/qr.h and
-include/qr_layer.h) for gfx950, and libqr_pattern.so, the benchmark's
+"""Build libqr.so (the HIP kernels and the C ABI of include/qr.h,
+include/qr_layer.h and include/qr_f8.h) for gfx950, and libqr_pattern.so, the benchmark's
 access-pattern reference (not part of the library's ABI).
 
 Flags that matter for the numerics: -ffp-contract=off (no fused multiply-add
@@ -17,7 +17,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libqr.so")
 SOURCES = [os.path.join(CSRC, f) for f in
-           ("qr_kernels.hip", "qr_rows.hip", "qr_gemm.hip", "qr_api.cpp", "qr_layer_api.cpp")]
+           ("qr_kernels.hip", "qr_rows.hip", "qr_gemm.hip", "qr_rows_f8.hip", "qr_gemm_f8.hip",
+            "qr_experts.hip", "qr_api.cpp", "qr_layer_api.cpp", "qr_f8_api.cpp")]
 PATTERN_LIB = os.path.join(PKG, "libqr_pattern.so")
 PATTERN_SOURCES = [os.path.join(CSRC, "qr_pattern.hip")]
 ARCH = os.environ.get("QR_OFFLOAD_ARCH", "gfx950")

@@ -26,68 +26,12 @@
 #include <utility>
 
 #include "qr.h"
-#include "qr_device.h"
+#include "qr_gemm_device.h"
 #include "qr_gemm_tiles.h"
 #include "qr_layer_internal.h"
 
 namespace qr {
 namespace {
-
-typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
-
-// 16 bytes from base + voff + soff to LDS byte lds + 16*lane, for every lane of
-// the wave, without passing through registers; s_waitcnt vmcnt covers it.  In
-// assembly since the compiler, where it cannot tell two LDS buffers apart,
-// would wait for the load before any LDS read: the caller waits.  It has no
-// output register, so nothing is written behind the compiler's back but LDS:
-// m0, which holds the LDS address, is an input that the compiler sets (the wait
-// state is the one that a load through m0 needs after that).
-// Once: past the caches, for what no other workgroup reads.
-template <bool Once>
-__device__ __forceinline__ void load_to_lds(i32x4 rsrc, uint32_t lds, uint32_t voff,
-                                            uint32_t soff) {
-  if constexpr (Once)
-    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
-                 :
-                 : "{m0}"(lds), "v"(voff), "s"(rsrc), "s"(soff)
-                 : "memory");
-  else
-    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :
-                 : "{m0}"(lds), "v"(voff), "s"(rsrc), "s"(soff)
-                 : "memory");
-}
-// A buffer that starts at p, for load_to_lds.  The wait states are those that
-// a memory instruction needs after a vector instruction (readfirstlane) wrote
-// its scalar operands: the compiler does not see the loads in the assembly.
-// Later changes of a buffer are scalar instructions, which need none.
-__device__ __forceinline__ i32x4 buffer_at(const void* p) {
-  const uint64_t a = (uint64_t)p;
-  const int lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
-  const int hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)) & 0xffff;
-  i32x4 r = {lo, hi, -1, 0x00027000};
-  asm volatile("s_nop 4" : "+s"(r));
-  return r;
-}
-// all of the buffer while s < steps, afterwards nothing (and nothing is fetched)
-__device__ __forceinline__ void end_buffer(i32x4& r, uint32_t s, uint32_t steps) {
-  int bytes;
-  asm("s_cmp_lt_u32 %1, %2\n\ts_cselect_b32 %0, -1, 0"
-      : "=s"(bytes)
-      : "s"(s), "s"(steps)
-      : "scc");
-  r[2] = bytes;
-}
-
-// The 16-byte piece v of a row, which starts at code k, with zeros past K.
-__device__ __forceinline__ i32x4 cut(i32x4 v, uint32_t k, uint32_t K) {
-#pragma unroll
-  for (int w = 0; w < 4; w++) {
-    const int left = (int)(K - k) - 4 * w;               // bytes of word w inside the row
-    v[w] = left >= 4 ? v[w] : left <= 0 ? 0 : (int)((uint32_t)v[w] & ((1u << (8 * left)) - 1u));
-  }
-  return v;
-}
 
 // scales and bias of W neighbouring channels
 template <int W>
@@ -111,39 +55,6 @@ __device__ __forceinline__ Channels<W> channels(const GemmArgs& g, uint32_t n) {
     ch.bias[e] = ch.biased ? ld16<D>(b16[at]) : 0.0f;
   }
   return ch;
-}
-
-// W/2 words of 16-bit values to c[m][n..]: one store inside the row
-template <int W, class V>
-__device__ __forceinline__ void store_row(const GemmArgs& g, uint32_t m, uint32_t n, const V& w) {
-  uint16_t* c = reinterpret_cast<uint16_t*>(g.c) + (size_t)m * g.ldc + n;
-  if (n + W <= g.N) {
-    __builtin_memcpy(c, &w, 2 * W);
-  } else {
-#pragma unroll 1
-    for (uint32_t e = 0; n + e < g.N; e++) {
-      uint32_t x = w[0];
-#pragma unroll
-      for (uint32_t k = 1; k < W / 2; k++) x = e / 2 == k ? w[k] : x;
-      c[e] = (uint16_t)(x >> (16 * (e % 2)));
-    }
-  }
-}
-
-// order of the tiles: see tile_of
-struct Grid {
-  uint32_t tm, tn, group;             // tiles along M and N; tile rows of a group
-};
-
-__device__ __forceinline__ void tile_of(const Grid& gr, uint32_t b, uint32_t& m, uint32_t& n) {
-  const uint32_t total = gr.tm * gr.tn, per = total / 8, extra = total % 8;
-  const uint32_t x = b % 8, i = b / 8;
-  const uint32_t t = x * per + (x < extra ? x : extra) + i;
-  const uint32_t g = t / (gr.group * gr.tn), r = t % (gr.group * gr.tn);
-  const uint32_t m0 = g * gr.group;
-  const uint32_t rows = gr.tm - m0 < gr.group ? gr.tm - m0 : gr.group;
-  m = m0 + r % rows;
-  n = r / rows;
 }
 
 // The sums of W waves, each FN blocks of 16 channels wide and `Apart` entries

@@ -1,0 +1,549 @@
+// qr_gemm_f8.hip -- gfx950 kernels of qr_gemm_f8 and qr_gemm_f8_grouped
+// (include/qr_f8.h): matrix products of E4M3FN codes with a scale for each block
+// of 128, the tokens in one group or grouped by expert.
+//
+// A block's sum is one matrix instruction (16x16x128): it starts from zero, and
+// its four results a lane are multiplied by the token's scale times the weights'
+// block scale and added to binary32 sums with one fused multiply-add each, while
+// the matrix unit works on the next.  Stages of the sum are therefore blocks.
+// Loads, rings, swizzle and the two kernels (k_split, k_tile) are as in
+// qr_gemm.hip; the tokens' scales pass through LDS beside the codes, the
+// weights' through the scalar cache.
+//
+// By experts: the grid has a workgroup for every tile that there may be; each
+// finds its expert and rows from the offsets.
+#include <type_traits>
+#include <utility>
+
+#include "qr_f8.h"
+#include "qr_f8_internal.h"
+#include "qr_gemm_device.h"
+#include "qr_gemm_f8_tiles.h"
+
+namespace qr {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+
+// 4 bytes a lane, as load_to_lds
+__device__ __forceinline__ void load_word_to_lds(i32x4 rsrc, uint32_t lds, uint32_t voff,
+                                                 uint32_t soff) {
+  asm volatile("s_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+               :
+               : "{m0}"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+               : "memory");
+}
+
+// 16x16 sums over the 128 codes of a block
+__device__ __forceinline__ f32x4 block_sum(const i32x4 (&b)[2], const i32x4 (&a)[2]) {
+  const i32x8 x = __builtin_shufflevector(b[0], b[1], 0, 1, 2, 3, 4, 5, 6, 7);
+  const i32x8 y = __builtin_shufflevector(a[0], a[1], 0, 1, 2, 3, 4, 5, 6, 7);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0,
+                                                          0, 0, 0, 0);
+}
+__device__ __forceinline__ void add_scaled(f32x4& acc, const f32x4& d, float s) {
+#pragma unroll
+  for (int e = 0; e < 4; e++) acc[e] = __builtin_fmaf(d[e], s, acc[e]);
+}
+
+typedef const __attribute__((address_space(4))) float* ConstF;
+__device__ __forceinline__ ConstF constant(const float* p) {
+  return (ConstF)(uintptr_t)p;
+}
+
+// what a workgroup works on
+struct Job {
+  uint32_t m0, end;                   // its first row, and the end of its expert's rows
+  uint32_t n0;
+  const uint8_t* b;
+  const float* sb;
+  const uint8_t* bias;
+};
+
+// Rows [lo, hi) of expert e.  Offsets are taken into 0..M, falling ones as equal.
+__device__ __forceinline__ void rows_of(const F8Args& g, uint32_t e, uint32_t& lo, uint32_t& hi) {
+  const int32_t x = g.offsets[e], y = g.offsets[e + 1], M = (int32_t)g.M;
+  const int32_t l = x < 0 ? 0 : x > M ? M : x, h = y < l ? l : y > M ? M : y;
+  lo = (uint32_t)l;
+  hi = (uint32_t)h;
+}
+
+// false: there is no such tile.  Every wave adds up the experts' tiles by itself,
+// 64 experts at a time.
+template <uint32_t BM, uint32_t BN, bool Grouped>
+__device__ __forceinline__ bool find_job(const F8Args& g, Grid gr, Job& job) {
+  uint32_t tm, tn;
+  job = Job{0, g.M, 0, g.b, g.sb, g.bias};
+  if constexpr (!Grouped) {
+    tile_of(gr, blockIdx.x, tm, tn);
+    job.m0 = tm * BM;
+  } else {
+    const uint32_t lane = threadIdx.x % 64;
+    const auto tiles_up_to = [&](uint32_t e0, uint32_t& lo, uint32_t& hi) {
+      lo = hi = 0;
+      if (e0 + lane < g.E) rows_of(g, e0 + lane, lo, hi);
+      uint32_t n = (hi - lo + BM - 1) / BM;
+#pragma unroll
+      for (uint32_t d = 1; d < 64; d *= 2) {
+        const uint32_t up = (uint32_t)__shfl_up((int)n, d);
+        if (lane >= d) n += up;
+      }
+      return n;
+    };
+    const auto at = [](uint32_t v, uint32_t from) {
+      return (uint32_t)__builtin_amdgcn_readlane((int)v, (int)from);
+    };
+    uint32_t lo, hi, n = tiles_up_to(0, lo, hi), total = at(n, 63), e0 = 0;
+    for (uint32_t e = 64; e < g.E; e += 64) {
+      uint32_t l, h;
+      total += at(tiles_up_to(e, l, h), 63);
+    }
+    gr.tm = total;
+    if (blockIdx.x >= total * gr.tn) return false;
+    tile_of(gr, blockIdx.x, tm, tn);
+    while (tm >= at(n, 63)) {              // ends: tm < total
+      tm -= at(n, 63);
+      e0 += 64;
+      n = tiles_up_to(e0, lo, hi);
+    }
+    const uint32_t in = (uint32_t)__builtin_ctzll(__ballot(n > tm));
+    const uint32_t first = in == 0 ? 0 : at(n, in - 1);
+    job.m0 = at(lo, in) + (tm - first) * BM;
+    job.end = at(hi, in);
+    const size_t e = e0 + in;
+    job.b += e * g.gb;
+    job.sb += e * g.gsb;
+    if (job.bias) job.bias += 2 * e * g.ldbias;
+  }
+  job.n0 = tn * BN;
+  return true;
+}
+
+// Where row m of a product lies in a: its number, counted from a's start (by
+// index) or from the tile's first row.  Rows past the last one are read as the
+// last one, an index outside a as row 0; what they give is not written.
+template <bool Grouped>
+__device__ __forceinline__ uint32_t row_of(const F8Args& g, const Job& job, uint32_t r) {
+  const uint32_t m = job.m0 + r < job.end ? job.m0 + r : job.end - 1;
+  if (Grouped && g.rows) {
+    const uint32_t at = (uint32_t)g.rows[m];
+    return at < g.tokens ? at : 0u;
+  }
+  return m - job.m0;
+}
+// whether row m of c takes a row of a
+template <bool Grouped>
+__device__ __forceinline__ bool real_row(const F8Args& g, uint32_t m) {
+  return !Grouped || !g.rows || (uint32_t)g.rows[m] < g.tokens;
+}
+template <bool Grouped>
+__device__ __forceinline__ size_t first_row(const F8Args& g, const Job& job) {
+  return Grouped && g.rows ? 0 : job.m0;
+}
+
+// A BM x BN tile to a workgroup of WM x WN waves, through a ring of S stages of
+// one block each.
+//
+// The tokens' scales come 8 blocks at a time (two 16-byte pieces a row), one load
+// a lane, into the one of two buffers that is not in use.
+template <int BM, int BN, int WM, int WN, int S, int D, bool Once, bool Grouped>
+__global__ __launch_bounds__(64 * WM * WN, 1) void k_tile_f8(F8Args g, Grid gr) {
+  constexpr int T = 64 * WM * WN;
+  constexpr int FM = BM / WM / 16, FN = BN / WN / 16;     // 16x16 blocks of a wave
+  constexpr int LA = BM * 8 / T, LB = BN * 8 / T;         // 16-byte pieces a lane loads a stage
+  constexpr uint32_t kStage = (BM + BN) * 8;              // pieces of a stage
+  constexpr uint32_t kChunk = 8;                          // blocks whose scales come together
+  static_assert(BN / WN <= 128 && 128 % (BN / WN) == 0 && BM * 2 <= T);
+  __shared__ i32x4 lds[S * kStage];
+  __shared__ __attribute__((aligned(16))) float lsa[2][BM * kChunk];
+  __shared__ float lbias[BN];
+
+  const uint32_t t = threadIdx.x, lane = t % 64, wave = __builtin_amdgcn_readfirstlane(t / 64);
+  Job job;
+  if (!find_job<BM, BN, Grouped>(g, gr, job)) return;
+  const uint32_t m0 = job.m0, n0 = job.n0;
+  const uint32_t K16 = (g.K + 15) & ~15u;
+  const uint32_t steps = (g.K + kStep - 1) / kStep;
+  const bool cut_last = g.K % kStep != 0;
+
+  // offsets of this lane's pieces in the stage at k; rows past the last one are
+  // read as the last one, pieces past a row's end as its last
+  uint32_t ra0[LA], va[LA], vb[LB];
+#pragma unroll
+  for (int i = 0; i < LA; i++) ra0[i] = row_of<Grouped>(g, job, (i * T + t) / 8) * (uint32_t)g.lda;
+  const auto offsets = [&](uint32_t k) {
+#pragma unroll
+    for (int i = 0; i < LA; i++) {
+      const uint32_t r = (i * T + t) / 8, c = 16 * (t % 8 ^ (r & 7));
+      va[i] = ra0[i] + (k + c < K16 ? c : K16 - 16 - k);
+    }
+#pragma unroll
+    for (int i = 0; i < LB; i++) {
+      const uint32_t r = (i * T + t) / 8, c = 16 * (t % 8 ^ ((r & 3) | (r >> 3 & 1) << 2));
+      const uint32_t row = n0 + r < g.N ? r : g.N - 1 - n0;
+      vb[i] = row * (uint32_t)g.ldb + (k + c < K16 ? c : K16 - 16 - k);
+    }
+  };
+  // Scales: place x of a row holds its piece x ^ (row & 1); lanes beyond the
+  // rows load what others load, to the same place.
+  const uint32_t srow = t / 2 % BM, spiece = (t ^ srow) & 1;
+  const uint32_t vs = row_of<Grouped>(g, job, srow) * (uint32_t)g.ldsa * 4;
+  const uint32_t last_piece = (steps + 3) / 4 - 1;
+  const auto lds_at = [](const void* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+  };
+  const uint32_t lds0 = lds_at(lds) + wave * 1024;
+  const uint32_t lsa0 = lds_at(lsa) + wave * 1024 % (BM * kChunk * 4);
+  const auto load_scales = [&](i32x4 rs, uint32_t chunk) {
+    const uint32_t piece = 2 * chunk + spiece;
+    load_to_lds<false>(rs, lsa0 + (chunk & 1) * (BM * kChunk * 4),
+                       vs + 16 * (piece < last_piece ? piece : last_piece), 0);
+  };
+  // piece-loads 0..LA+LB-1 of the stage at code k into the buffer at byte `to`
+  const auto load = [&](int i, i32x4 ra, i32x4 rb, uint32_t k, uint32_t to) {
+    if (i < LA) load_to_lds<false>(ra, lds0 + to + i * T * 16, va[i < LA ? i : 0], k);
+    else load_to_lds<Once>(rb, lds0 + to + (BM * 8 + (i - LA) * T) * 16, vb[i < LA ? 0 : i - LA], k);
+  };
+  // zeros for the codes of the last stage that lie past K, of a and b: either may
+  // hold NaN codes there
+  const auto cut_stage = [&](uint32_t at_stage) {
+    const uint32_t k0 = (steps - 1) * kStep;
+#pragma unroll 1
+    for (uint32_t x = t; x < kStage; x += T) {
+      const uint32_t r = x < BM * 8 ? x / 8 : (x - BM * 8) / 8;
+      const uint32_t turn = x < BM * 8 ? r & 7 : (r & 3) | (r >> 3 & 1) << 2;
+      const uint32_t k = k0 + 16 * (x % 8 ^ turn);
+      i32x4* at = lds + at_stage + x;
+      if (k + 16 > g.K) *at = cut(*at, k, g.K);
+    }
+    __syncthreads();
+  };
+  // waits for all but this wave's youngest loads and its LDS reads, then everyone's
+  constexpr int kYoung = (S - 2) * (LA + LB);
+  static_assert(kYoung + LA + LB < 64, "s_waitcnt counts to 63");
+  const auto arrived = [](auto left) {
+    constexpr int n = decltype(left)::value;
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((n & 15) | (n >> 4) << 14 | 0x0070);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
+  const uint32_t p = lane % 16, q = lane / 16;
+  const uint32_t wm = wave % WM * (BM / WM), wn = wave / WM * (BN / WN);
+  const uint32_t at = q ^ (lane & 7);
+  uint32_t xa = (wm + p) * 8 + at, xb = BM * 8 + (wn + p / 4 * 8 + p % 4) * 8 + at;
+  f32x4 acc[FM][FN] = {};
+  i32x4 fa[FM][2], fb[2][2];
+  float s[FM], sa[FM];
+  const auto read_a = [&](int i) {
+#pragma unroll
+    for (int h = 0; h < 2; h++) fa[i][h] = lds[(xa ^ (4 * h)) + i * 128];
+  };
+  const auto read_b = [&](int j) {
+#pragma unroll
+    for (int h = 0; h < 2; h++) fb[j % 2][h] = lds[(xb ^ (4 * h)) + (j / 2 * 32 + j % 2 * 4) * 8];
+  };
+  // the tokens' scales of a block
+  const auto read_scales = [&](uint32_t step) {
+    const float* const from = lsa[step / kChunk & 1] + (wm + p) * kChunk +
+                              ((step % kChunk / 4 ^ p) & 1) * 4 + step % 4;
+#pragma unroll
+    for (int i = 0; i < FM; i++) sa[i] = from[i * 16 * kChunk];
+  };
+  const uint32_t nb = (n0 + wn < g.N ? n0 + wn : g.N - 1) / 128;
+  const ConstF sbp = constant(job.sb + (size_t)nb * g.ldsb);
+
+  // the bias, for the end
+  const uint16_t* bias = reinterpret_cast<const uint16_t*>(job.bias);
+  for (uint32_t x = t; x < BN; x += T)
+    lbias[x] = bias ? ld16<D>(bias[n0 + x < g.N ? n0 + x : g.N - 1]) : 0.0f;
+
+  const size_t from = first_row<Grouped>(g, job);
+  i32x4 ra = buffer_at(g.a + from * g.lda), rb = buffer_at(job.b + (size_t)n0 * g.ldb);
+  const i32x4 rs = buffer_at(g.sa + from * g.ldsa);
+  load_scales(rs, 0);
+  load_scales(rs, 1);
+  offsets(0);
+#pragma unroll
+  for (uint32_t s = 0; s < S; s++) {
+    if (s + 1 == steps && cut_last) offsets(s * kStep);
+    end_buffer(ra, s, steps);
+    end_buffer(rb, s, steps);
+#pragma unroll
+    for (int i = 0; i < LA + LB; i++) load(i, ra, rb, s < steps ? s * kStep : 0u, s * kStage * 16);
+  }
+  float sb = sbp[0];
+  arrived(std::integral_constant<int, kYoung + LA + LB>{});
+  if (steps == 1 && cut_last) cut_stage(0);
+  read_b(0);
+#pragma unroll
+  for (int i = 0; i < FM; i++) read_a(i);
+  read_scales(0);
+
+  // One stage a turn: FN columns of FM products, the results of one joined to
+  // the sums while the next ones run, the next column's codes read meanwhile.
+  // Before the last column the next stage has arrived and everyone has read this
+  // one: then the next one's first codes are read, each over the one just used,
+  // and the stage S after this one is loaded over it, over the next columns.
+  constexpr int kProducts = FM * FN, kLag = 2;
+  f32x4 d[4];
+  uint32_t to = 0;                           // this stage's place, in pieces
+  uint32_t old_to = 0;
+  for (uint32_t step = 0; step < steps; step++) {
+#pragma unroll
+    for (int i = 0; i < FM; i++) s[i] = sa[i] * sb;
+    const uint32_t next = to == (S - 1) * kStage ? 0 : to + kStage;
+#pragma unroll
+    for (int j = 0; j < FN; j++) {
+      if (j + 1 < FN) read_b(j + 1);
+      if (j + 2 == FN) {
+        const uint32_t after = step + 1 < steps ? step + 1 : step;
+        read_scales(after);
+        sb = sbp[after];
+      }
+      if (j + 1 == FN) {
+        arrived(std::integral_constant<int, kYoung>{});
+        if (step + 2 == steps && cut_last) cut_stage(next);
+        if (step + 1 + S == steps && cut_last) offsets((step + S) * kStep);
+        end_buffer(ra, step + S, steps);
+        end_buffer(rb, step + S, steps);
+        xa += next - to;
+        xb += next - to;
+        old_to = to;
+        if ((step + 1) % kChunk == 0) load_scales(rs, step / kChunk + 2);
+      }
+#pragma unroll
+      for (int i = 0; i < FM; i++) {
+        const int x = j * FM + i;
+        __builtin_amdgcn_sched_barrier(0);
+        d[x % 4] = block_sum(fb[j % 2], fa[i]);
+        if (j + 1 == FN) {
+          if (i == 0) read_b(0);
+          read_a(i);
+        }
+        if (x >= kLag) {
+          const int y = x - kLag;
+          add_scaled(acc[y % FM][y / FM], d[y % 4], s[y % FM]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+#pragma unroll
+    for (int y = kProducts - kLag; y < kProducts; y++) add_scaled(acc[y % FM][y / FM], d[y % 4], s[y % FM]);
+#pragma unroll
+    for (int i = 0; i < LA + LB; i++)
+      load(i, ra, rb, step + S < steps ? (step + S) * kStep : 0u, old_to * 16);
+    to = next;
+  }
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0f70);        // nothing may still be on its way to LDS
+
+  // this lane holds, of token wm + 16i + p, the channels wn + 32(j/2) + 8q +
+  // 4(j%2) + e: 8 neighbours for two j
+#pragma unroll
+  for (int i = 0; i < FM; i++) {
+    const uint32_t m = m0 + wm + 16 * i + p;
+    if (m >= job.end) continue;
+    const bool real = real_row<Grouped>(g, m);
+#pragma unroll
+    for (int j = 0; j < FN; j += 2) {
+      const uint32_t x = wn + 16 * j + 8 * q;
+      u32x4 w;
+#pragma unroll
+      for (int h = 0; h < 4; h++) {
+        const f32x4& v = acc[i][j + h / 2];
+        const int e = h % 2 * 2;
+        w[h] = real ? st16x2<D>(v[e] + lbias[x + 2 * h], v[e + 1] + lbias[x + 2 * h + 1]) : 0u;
+      }
+      store_row<8>(g, m, n0 + x, w);
+    }
+  }
+}
+
+// A block of BM tokens by BN channels to a workgroup, whose W waves share the
+// sum: wave w takes blocks w, w + W, ... through a ring of S stages of its own in
+// LDS, the tokens' scales beside the codes.
+constexpr uint32_t kApart = 2;               // stages from one tile's start to its neighbour's
+
+template <int BM, int BN, int W, int S, int D, bool Once, bool Grouped>
+__global__ __launch_bounds__(64 * W) void k_split_f8(F8Args g, Grid gr) {
+  constexpr int FM = (BM + 15) / 16, FN = BN / 16;
+  constexpr int LA = BM / 8, LB = BN / 8, L = LA + LB + 1;  // loads of a stage
+  constexpr uint32_t kScales = (BM + BN) * 8;             // where the scales lie
+  constexpr uint32_t kStage = kScales + 16;               // pieces of a stage
+  static_assert(FM * FN * 64 <= S * kStage && (S - 1) * L < 64 && BM <= 64 && BN <= 128);
+  __shared__ i32x4 lds[W * S * kStage];
+  const uint32_t t = threadIdx.x, lane = t % 64, wave = __builtin_amdgcn_readfirstlane(t / 64);
+  Job job;
+  if (!find_job<BM, BN, Grouped>(g, gr, job)) return;
+  const uint32_t n0 = job.n0;
+  const uint32_t K16 = (g.K + 15) & ~15u;
+  const uint32_t steps = (g.K + kStep - 1) / kStep;
+  const bool cut_last = g.K % kStep != 0;
+  uint32_t ra0[LA], va[LA], vb[LB];
+#pragma unroll
+  for (int i = 0; i < LA; i++) ra0[i] = row_of<Grouped>(g, job, i * 8 + lane / 8) * (uint32_t)g.lda;
+  const uint32_t vs = row_of<Grouped>(g, job, lane < BM ? lane : BM - 1) * (uint32_t)g.ldsa * 4;
+  const auto offsets = [&](uint32_t k) {
+    const uint32_t c = 16 * (lane % 8 ^ lane / 8), at = k + c < K16 ? c : K16 - 16 - k;
+#pragma unroll
+    for (int i = 0; i < LA; i++) va[i] = ra0[i] + at;
+#pragma unroll
+    for (int i = 0; i < LB; i++) {
+      const uint32_t r = i * 8 + lane / 8;
+      vb[i] = (n0 + r < g.N ? r : g.N - 1 - n0) * (uint32_t)g.ldb + at;
+    }
+  };
+  i32x4* const ring = lds + wave * S * kStage;
+  const uint32_t ring0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds +
+                         wave * S * kStage * 16;
+  const size_t from = first_row<Grouped>(g, job);
+  i32x4 ra = buffer_at(g.a + from * g.lda), rb = buffer_at(job.b + (size_t)n0 * g.ldb);
+  i32x4 rs = buffer_at(g.sa + from * g.ldsa);
+  const ConstF sbp = constant(job.sb + (size_t)(n0 / 128) * g.ldsb);
+  // block s into slot `to`; past the last block from an empty buffer, from which
+  // nothing is fetched
+  const uint32_t rest = steps > 1 ? steps - 1 : 1;        // the last one stays last
+  const uint32_t turn = (uint32_t)__builtin_amdgcn_readfirstlane((int)(n0 / BN * kApart % rest));
+  const auto block_of = [&](uint32_t s) {
+    const uint32_t at = s + turn < rest ? s + turn : s + turn - rest;
+    return s + 1 >= steps ? (s < steps ? s : 0u) : at;
+  };
+  const auto load = [&](uint32_t s, uint32_t to) {
+    const uint32_t at = block_of(s), k = at * kStep;
+    end_buffer(ra, s, steps);
+    end_buffer(rb, s, steps);
+    end_buffer(rs, s, steps);
+    if (s + 1 == steps && cut_last) offsets(k);
+#pragma unroll
+    for (int i = 0; i < LB; i++)
+      load_to_lds<Once>(rb, ring0 + (to * kStage + BM * 8 + i * 64) * 16, vb[i], k);
+#pragma unroll
+    for (int i = 0; i < LA; i++)
+      load_to_lds<false>(ra, ring0 + (to * kStage + i * 64) * 16, va[i], k);
+    load_word_to_lds(rs, ring0 + (to * kStage + kScales) * 16, vs, 4 * at);
+  };
+  const uint32_t p = lane % 16, q = lane / 16;
+  const uint32_t x0 = p * 8 + (q ^ (p & 7)), xa = BM < 16 ? x0 & 63 : x0;
+  f32x4 acc[FM][FN] = {};
+  offsets(0);
+#pragma unroll
+  for (uint32_t i = 0; i < S; i++) load(wave + i * W, i);
+  float sb = sbp[block_of(wave)];
+  uint32_t to = 0;
+#pragma unroll 1
+  for (uint32_t s = wave; s < steps; s += W) {
+    constexpr int n = (S - 1) * L;
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((n & 15) | (n >> 4) << 14 | 0x0f70);
+    asm volatile("" ::: "memory");
+    i32x4* const at = ring + to * kStage;
+    if (s + 1 == steps && cut_last) {
+      // zeros for the codes past K, of a and b: either may hold NaN codes there
+      const uint32_t k = s * kStep + 16 * (lane % 8 ^ lane / 8);
+#pragma unroll
+      for (int i = 0; i < LA + LB; i++)
+        if (k + 16 > g.K) at[i * 64 + lane] = cut(at[i * 64 + lane], k, g.K);
+    }
+    i32x4 fa[FM][2], fb[FN][2];
+    float sa[FM];
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+#pragma unroll
+      for (int j = 0; j < FN; j++) fb[j][h] = at[BM * 8 + j * 128 + (x0 ^ (4 * h))];
+#pragma unroll
+      for (int i = 0; i < FM; i++) fa[i][h] = at[i * 128 + (xa ^ (4 * h))];
+    }
+    const float* const scales = reinterpret_cast<const float*>(at + kScales);
+#pragma unroll
+    for (int i = 0; i < FM; i++) sa[i] = scales[BM < 16 ? p % BM : 16 * i + p] * sb;
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xc07f);      // the slot is read: it may be loaded again
+    asm volatile("" ::: "memory");
+    load(s + S * W, to);
+    sb = sbp[block_of(s + W)];
+    __builtin_amdgcn_sched_barrier(0);
+    f32x4 d[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; i++)
+#pragma unroll
+      for (int j = 0; j < FN; j++) d[i][j] = block_sum(fb[j], fa[i]);
+#pragma unroll
+    for (int i = 0; i < FM; i++)
+#pragma unroll
+      for (int j = 0; j < FN; j++) add_scaled(acc[i][j], d[i][j], sa[i]);
+    to = to + 1 == S ? 0 : to + 1;
+  }
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0f70);        // nothing may still be on its way to LDS
+  asm volatile("" ::: "memory");
+  f32x4* const sums = reinterpret_cast<f32x4*>(lds);
+#pragma unroll
+  for (int i = 0; i < FM; i++)
+#pragma unroll
+    for (int j = 0; j < FN; j++) sums[wave * S * kStage + (i * FN + j) * 64 + lane] = acc[i][j];
+  __syncthreads();
+  // the waves' sums, in their order: entry x holds 4 neighbouring channels of one
+  // token
+  for (uint32_t x = t; x < FM * FN * 64; x += 64 * W) {
+    const uint32_t f = x / 64, m = job.m0 + f / FN * 16 + x % 16;
+    const uint32_t n = n0 + f % FN * 16 + x % 64 / 16 * 4;
+    f32x4 sum = sums[x];
+#pragma unroll
+    for (int w = 1; w < W; w++) sum += sums[w * S * kStage + x];
+    if (m < job.end && n < g.N && (BM >= 16 || x % 16 < BM)) {
+      const uint16_t* const bias = reinterpret_cast<const uint16_t*>(job.bias);
+      if (bias)
+#pragma unroll
+        for (uint32_t e = 0; e < 4; e++) sum[e] += ld16<D>(bias[n + e < g.N ? n + e : g.N - 1]);
+      u32x2 v = {0u, 0u};
+      if (real_row<Grouped>(g, m))
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) v[e / 2] = st16x2<D>(sum[e], sum[e + 1]);
+      store_row<4>(g, m, n, v);
+    }
+  }
+}
+
+template <int I>
+hipError_t launch_tile(int dtype, const F8Args& g, hipStream_t st) {
+  constexpr Tile t = kF8Tiles[I];
+  const Grid gr{f8_tile_rows(t.bm, g.M, g.E), (g.N + t.bn - 1) / t.bn, t.group};
+  const dim3 grid(gr.tm * gr.tn), block(64 * t.wm * (t.wn ? t.wn : 1));
+  const auto kernel = [&](auto d, auto once, auto grouped) {
+    constexpr int D = decltype(d)::value;
+    constexpr bool Once = decltype(once)::value, Grouped = decltype(grouped)::value;
+    if constexpr (t.wn == 0) k_split_f8<t.bm, t.bn, t.wm, t.stages, D, Once, Grouped><<<grid, block, 0, st>>>(g, gr);
+    else k_tile_f8<t.bm, t.bn, t.wm, t.wn, t.stages, D, Once, Grouped><<<grid, block, 0, st>>>(g, gr);
+  };
+  const auto of_type = [&](auto d) {
+    if (g.E == 0) {
+      if constexpr (t.bm <= 8) kernel(d, std::true_type{}, std::false_type{});   // never more tokens
+      else if (gr.tm == 1) kernel(d, std::true_type{}, std::false_type{});
+      else kernel(d, std::false_type{}, std::false_type{});
+    } else {
+      kernel(d, std::false_type{}, std::true_type{});
+    }
+  };
+  if (dtype == kF16) of_type(std::integral_constant<int, kF16>{});
+  else of_type(std::integral_constant<int, kBF16>{});
+  return hipGetLastError();
+}
+
+using Launch = hipError_t (*)(int, const F8Args&, hipStream_t);
+template <int... I>
+Launch launch_of(int tile, std::integer_sequence<int, I...>) {
+  static constexpr Launch table[] = {launch_tile<I>...};
+  return table[tile];
+}
+
+}  // namespace
+
+hipError_t launch_gemm_f8(int dtype, const F8Args& g, hipStream_t st) {
+  return launch_of(choose_f8_tile(g.M, g.N, g.K, g.E),
+                   std::make_integer_sequence<int, kF8TileCount>{})(dtype, g, st);
+}
+
+}  // namespace qr

@@ -1,5 +1,5 @@
-"""Python binding of the C ABI in include/qr.h and include/qr_layer.h (argument
-marshalling only).
+"""Python binding of the C ABI in include/qr.h, include/qr_layer.h and
+include/qr_f8.h (argument marshalling only).
 
 Every function has the name of the C entry point it calls and takes torch
 tensors on the GPU; all work happens in libqr.so's HIP kernels, on the current
@@ -17,6 +17,7 @@ import torch
 QR_FP, QR_Q8, QR_Q6, QR_Q4, QR_FP8 = 0, 1, 2, 3, 5
 QR_Q8_ASYM, QR_Q6_ASYM, QR_Q4_ASYM = 9, 10, 11
 QR_FP16, QR_BF16, QR_BF16_VIA_FP16 = 0, 1, 2
+QR_FP32 = 3                                # of a router's logits only
 CODECS = (QR_FP, QR_FP8, QR_Q8, QR_Q6, QR_Q4, QR_Q8_ASYM, QR_Q6_ASYM, QR_Q4_ASYM)
 CODEC_NAMES = {QR_FP: "fp", QR_Q8: "q8", QR_Q6: "q6", QR_Q4: "q4", QR_FP8: "fp8",
                QR_Q8_ASYM: "q8a", QR_Q6_ASYM: "q6a", QR_Q4_ASYM: "q4a"}
@@ -62,6 +63,15 @@ def _load():
         "qr_silu_mul_q8": (i32, [i32, P, sz, sz, sz, P, sz, P, P]),
         "qr_gemm_i8": (i32, [i32, P, sz, P, P, sz, P, P, sz, sz, sz, P, sz, P, sz, P]),
         "qr_gemm_i8_workspace_bytes": (sz, [sz, sz, sz]),
+        "qr_add_rmsnorm_f8": (i32, [i32, P, sz, P, sz, P, f32, sz, sz, P, sz, P, sz, P, sz, P, sz,
+                                    P]),
+        "qr_silu_mul_f8": (i32, [i32, P, sz, sz, sz, P, sz, P, sz, P]),
+        "qr_gemm_f8": (i32, [i32, P, sz, P, sz, P, sz, P, sz, P, sz, sz, sz, P, sz, P]),
+        "qr_gemm_f8_grouped": (i32, [i32, P, sz, P, sz, P, sz, P, sz, sz, P, sz, sz, P, sz, P, sz,
+                                     sz, sz, sz, P, sz, P]),
+        "qr_route": (i32, [i32, P, sz, sz, sz, sz, i32, P, P, P, P, P, P, sz, P]),
+        "qr_route_workspace_bytes": (sz, [sz, sz, sz]),
+        "qr_combine": (i32, [i32, P, sz, sz, P, P, sz, sz, sz, P, sz, P, sz, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -75,7 +85,9 @@ EXPORTS = ("qr_wire_bytes", "qr_sim_workspace_bytes", "qr_recv_bytes", "qr_quant
            "qr_reduce_recv", "qr_gather_stage2",
            "qr_allreduce_sim", "qr_allreduce_oneshot", "qr_allreduce_sim_noalloc",
            "qr_last_error", "qr_add_rmsnorm_q8", "qr_gather_add_rmsnorm_q8", "qr_silu_mul_q8",
-           "qr_gemm_i8", "qr_gemm_i8_workspace_bytes")
+           "qr_gemm_i8", "qr_gemm_i8_workspace_bytes", "qr_add_rmsnorm_f8", "qr_silu_mul_f8",
+           "qr_gemm_f8", "qr_gemm_f8_grouped", "qr_route", "qr_route_workspace_bytes",
+           "qr_combine")
 
 
 def _check(rc):
@@ -445,3 +457,182 @@ def alloc_q8(M, d, device="cuda"):
     16 bytes as qr_gemm_i8 reads them, and for the M scales."""
     q = torch.empty(M, -(-d // 16) * 16, dtype=torch.int8, device=device)[:, :d]
     return q, torch.empty(M, dtype=torch.float32, device=device)
+
+
+# ---------------------------------------------------------------------------
+# the operators in 8-bit floating point, dense and by experts (include/qr_f8.h)
+
+_F8 = torch.float8_e4m3fn
+_LOGITS = {torch.float16: QR_FP16, torch.bfloat16: QR_BF16, torch.float32: QR_FP32}
+
+
+def _blocks(n):
+    return -(-n // 128)
+
+
+def _pieces(what, t, rows, cols, dtype, dev, piece):
+    """A matrix whose rows are read in whole pieces of `piece` elements (16
+    bytes), the last one's padding inside the tensor's storage."""
+    ld = _mat(what, t, rows, cols, dtype, dev)
+    padded = -(-cols // piece) * piece
+    if rows == 1:
+        ld = padded
+    if cols % piece and rows > 0 and ((t.storage_offset() + (rows - 1) * ld + padded)
+                                      * t.element_size() > t.untyped_storage().nbytes()):
+        raise ValueError("%s: the padding of its last row up to a multiple of %d is outside its "
+                         "storage (alloc_f8 makes room for it)" % (what, piece))
+    return ld
+
+
+def qr_add_rmsnorm_f8(x, residual, weight, eps, h, y, q, scales, stream=None):
+    """h = x + residual; q, scales = the e4m3 codes and block scales of h's
+    root-mean-square norm times weight; y (or None) these values in 16 bits.
+    residual and h may be one tensor (updated in place), or both None (h = x).
+    Matrices are [M, d] with contiguous rows, scales [M, ceil(d/128)] float32."""
+    M, d = _matrix_shape("x", x)
+    code = _type16(x, "x")
+    dev = _device(x, "x")
+    ldx = _ld("x", x, M, d)
+    ldr = _mat("residual", residual, M, d, x.dtype, dev) if residual is not None else 0
+    ldh = _mat("h", h, M, d, x.dtype, dev) if h is not None else 0
+    ldy = _mat("y", y, M, d, x.dtype, dev) if y is not None else 0
+    _check(LIB.qr_add_rmsnorm_f8(
+        code, x.data_ptr(), ldx, residual.data_ptr() if residual is not None else None, ldr,
+        _vec("weight", weight, d, x.dtype, dev), eps, M, d,
+        h.data_ptr() if h is not None else None, ldh, y.data_ptr() if y is not None else None, ldy,
+        q.data_ptr(), _mat("q", q, M, d, _F8, dev), scales.data_ptr(),
+        _mat("scales", scales, M, _blocks(d), torch.float32, dev), _stream_on(dev, stream)))
+    return h, y, q, scales
+
+
+def qr_silu_mul_f8(gu, q, scales, stream=None):
+    """q, scales = the e4m3 codes and block scales of silu(gate) * up, where a
+    row of gu ([M, 2d]) holds the d gate values and then the d up values."""
+    M, d2 = _matrix_shape("gu", gu)
+    if d2 % 2 != 0:
+        raise ValueError("gu has rows of %d values: gate and up differ in length" % d2)
+    d = d2 // 2
+    code = _type16(gu, "gu")
+    dev = _device(gu, "gu")
+    _check(LIB.qr_silu_mul_f8(code, gu.data_ptr(), _ld("gu", gu, M, d2), M, d, q.data_ptr(),
+                              _mat("q", q, M, d, _F8, dev), scales.data_ptr(),
+                              _mat("scales", scales, M, _blocks(d), torch.float32, dev),
+                              _stream_on(dev, stream)))
+    return q, scales
+
+
+def qr_gemm_f8(a, sa, b, sb, c, bias=None, stream=None):
+    """c = a @ b^T (+ bias) of e4m3 codes, rounded once to c's type.  a: [M, K]
+    and sa its [M, ceil(K/128)] float32 block scales, b: [N, K] and sb its
+    [ceil(N/128), ceil(K/128)] scales of blocks of 128 x 128."""
+    M, K = _matrix_shape("a", a)
+    N = _matrix_shape("b", b)[0]
+    code = _type16(c, "c")
+    dev = _device(c, "c")
+    kb = _blocks(K)
+    _check(LIB.qr_gemm_f8(
+        code, a.data_ptr(), _pieces("a", a, M, K, _F8, dev, 16), sa.data_ptr(),
+        _pieces("sa", sa, M, kb, torch.float32, dev, 4), b.data_ptr(),
+        _pieces("b", b, N, K, _F8, dev, 16), sb.data_ptr(),
+        _mat("sb", sb, _blocks(N), kb, torch.float32, dev),
+        _vec("bias", bias, N, c.dtype, dev) if bias is not None else None, M, N, K, c.data_ptr(),
+        _mat("c", c, M, N, c.dtype, dev), _stream_on(dev, stream)))
+    return c
+
+
+def qr_gemm_f8_grouped(a, sa, b, sb, offsets, c, rows=None, bias=None, stream=None):
+    """The products of E experts: rows offsets[e] to offsets[e + 1] of c ([M, N])
+    are those of a, or with `rows` ([M] int32) row i is a's row rows[i], times
+    b[e]^T (+ bias[e]).  b: [E, N, K] e4m3 codes, sb: [E, ceil(N/128),
+    ceil(K/128)], bias: [E, N], offsets: [E + 1] int32 on the GPU."""
+    tokens, K = _matrix_shape("a", a)
+    M, N = _matrix_shape("c", c)
+    code = _type16(c, "c")
+    dev = _device(c, "c")
+    kb = _blocks(K)
+    for what, t in (("b", b), ("sb", sb)):
+        if t.dim() != 3:
+            raise ValueError("%s has %d dimensions: one matrix for each expert expected"
+                             % (what, t.dim()))
+    E = b.shape[0]
+    if sb.shape[0] != E:
+        raise ValueError("sb holds %d experts' scales: %d expected" % (sb.shape[0], E))
+    if E == 0:
+        raise ValueError("b holds no expert")
+    if rows is None and tokens != M:
+        raise ValueError("a has %d rows, c %d" % (tokens, M))
+    # the padding that may be missing is that of the last expert's last row
+    ldb = _pieces("b", b[-1], N, K, _F8, dev, 16)
+    ldsb = _mat("sb", sb[0], _blocks(N), kb, torch.float32, dev)
+    ldbias = _mat("bias", bias, E, N, c.dtype, dev) if bias is not None else 0
+    _check(LIB.qr_gemm_f8_grouped(
+        code, a.data_ptr(), _pieces("a", a, tokens, K, _F8, dev, 16), sa.data_ptr(),
+        _pieces("sa", sa, tokens, kb, torch.float32, dev, 4),
+        _vec("rows", rows, M, torch.int32, dev) if rows is not None else None, tokens,
+        b.data_ptr(), ldb, b.stride(0) if E > 1 else 0, sb.data_ptr(), ldsb,
+        sb.stride(0) if E > 1 else 0, bias.data_ptr() if bias is not None else None, ldbias,
+        _vec("offsets", offsets, E + 1, torch.int32, dev), E, M, N, K, c.data_ptr(),
+        _mat("c", c, M, N, c.dtype, dev), _stream_on(dev, stream)))
+    return c
+
+
+def qr_route(logits, weights, experts, offsets, rows, place, renormalize=False, workspace=None,
+             stream=None):
+    """The k experts of the largest logits ([T, E]) of every token, in falling
+    order: experts [T, k] int32 and their softmax weights [T, k] float32 (over all
+    experts, or with renormalize over the k); the rows sorted by expert: offsets
+    [E + 1], rows [T * k] (each row's token) and place [T, k] (each choice's row),
+    int32.  workspace: alloc_route_workspace(T, E, k)."""
+    T, E = _matrix_shape("logits", logits)
+    code = _LOGITS.get(logits.dtype)
+    if code is None:
+        raise TypeError("logits are %s: float16, bfloat16 or float32 expected" % logits.dtype)
+    dev = _device(logits, "logits")
+    k = _matrix_shape("weights", weights)[1]
+    for what, t, dtype in (("weights", weights, torch.float32), ("experts", experts, torch.int32),
+                           ("place", place, torch.int32)):
+        _mat(what, t, T, k, dtype, dev)
+        _vec(what, t, T * k, dtype, dev)
+    _check(LIB.qr_route(
+        code, logits.data_ptr(), _ld("logits", logits, T, E), T, E, k, int(bool(renormalize)),
+        weights.data_ptr(), experts.data_ptr(), _vec("offsets", offsets, E + 1, torch.int32, dev),
+        _vec("rows", rows, T * k, torch.int32, dev), place.data_ptr(),
+        workspace.data_ptr() if workspace is not None else None, _workspace_bytes(workspace, dev),
+        _stream_on(dev, stream)))
+    return weights, experts, offsets, rows, place
+
+
+def qr_combine(c, place, weights, y, addend=None, stream=None):
+    """y[t] = sum_j weights[t][j] * c[place[t][j]] (+ addend[t]).  c: [R, d],
+    place [T, k] int32 (places outside c add nothing), weights [T, k] float32,
+    y and addend [T, d]; addend may be y itself."""
+    R, d = _matrix_shape("c", c)
+    code = _type16(c, "c")
+    dev = _device(y, "y")
+    T, k = _matrix_shape("place", place)
+    _mat("weights", weights, T, k, torch.float32, dev)
+    lda = _mat("addend", addend, T, d, c.dtype, dev) if addend is not None else 0
+    _check(LIB.qr_combine(
+        code, c.data_ptr(), _mat("c", c, R, d, c.dtype, dev), R,
+        _vec("place", place, T * k, torch.int32, dev),
+        _vec("weights", weights, T * k, torch.float32, dev), T, k, d,
+        addend.data_ptr() if addend is not None else None, lda, y.data_ptr(),
+        _mat("y", y, T, d, c.dtype, dev), _stream_on(dev, stream)))
+    return y
+
+
+def qr_route_workspace_bytes(T, E, k):
+    return LIB.qr_route_workspace_bytes(T, E, k)
+
+
+def alloc_route_workspace(T, E, k, device="cuda"):
+    """Device memory for qr_route's workspace (None where it needs none)."""
+    n = qr_route_workspace_bytes(T, E, k)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def alloc_f8(M, d, device="cuda"):
+    """Device buffers for M rows of d e4m3 codes and for their block scales, each
+    row starting at a multiple of 16 bytes as qr_gemm_f8 reads them."""
+    q = torch.empty(M, -(-d // 16) * 16, dtype=_F8, device=device)[:, :d]
+    return q, torch.empty(M, -(-_blocks(d) // 4) * 4, dtype=torch.float32, device=device)[:, :_blocks(d)]
