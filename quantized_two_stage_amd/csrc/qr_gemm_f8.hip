@@ -35,6 +35,11 @@ __device__ __forceinline__ void load_word_to_lds(i32x4 rsrc, uint32_t lds, uint3
                : "memory");
 }
 
+// The compiler may move what makes v no further down than here.  Left alone it
+// gathers the additions of a whole stage behind its last product, with all the
+// products' results held until then (256x256: 128 registers spilled).
+__device__ __forceinline__ void here(f32x4& v) { asm volatile("" : "+v"(v)); }
+
 // 16x16 sums over the 128 codes of a block
 __device__ __forceinline__ f32x4 block_sum(const i32x4 (&b)[2], const i32x4 (&a)[2]) {
   const i32x8 x = __builtin_shufflevector(b[0], b[1], 0, 1, 2, 3, 4, 5, 6, 7);
@@ -148,8 +153,9 @@ __device__ __forceinline__ size_t first_row(const F8Args& g, const Job& job) {
 // The tokens' scales come 8 blocks at a time (two 16-byte pieces a row), one load
 // a lane, into the one of two buffers that is not in use.
 template <int BM, int BN, int WM, int WN, int S, int D, bool Once, bool Grouped>
-__global__ __launch_bounds__(64 * WM * WN, 1) void k_tile_f8(F8Args g, Grid gr) {
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_tile_f8(F8Args g, Grid gr) {
   constexpr int T = 64 * WM * WN;
+  constexpr bool Turns = S == 2 && T == 512;
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16;     // 16x16 blocks of a wave
   constexpr int LA = BM * 8 / T, LB = BN * 8 / T;         // 16-byte pieces a lane loads a stage
   constexpr uint32_t kStage = (BM + BN) * 8;              // pieces of a stage
@@ -157,7 +163,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_tile_f8(F8Args g, Grid gr) 
   static_assert(BN / WN <= 128 && 128 % (BN / WN) == 0 && BM * 2 <= T);
   __shared__ i32x4 lds[S * kStage];
   __shared__ __attribute__((aligned(16))) float lsa[2][BM * kChunk];
-  __shared__ float lbias[BN];
+  __shared__ float lsb[2][T], lbias[BN];
 
   const uint32_t t = threadIdx.x, lane = t % 64, wave = __builtin_amdgcn_readfirstlane(t / 64);
   Job job;
@@ -206,44 +212,49 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_tile_f8(F8Args g, Grid gr) 
     else load_to_lds<Once>(rb, lds0 + to + (BM * 8 + (i - LA) * T) * 16, vb[i < LA ? 0 : i - LA], k);
   };
   // zeros for the codes of the last stage that lie past K, of a and b: either may
-  // hold NaN codes there
+  // hold NaN codes there.  Every lane's own pieces, once they have arrived.
   const auto cut_stage = [&](uint32_t at_stage) {
     const uint32_t k0 = (steps - 1) * kStep;
-#pragma unroll 1
-    for (uint32_t x = t; x < kStage; x += T) {
-      const uint32_t r = x < BM * 8 ? x / 8 : (x - BM * 8) / 8;
-      const uint32_t turn = x < BM * 8 ? r & 7 : (r & 3) | (r >> 3 & 1) << 2;
-      const uint32_t k = k0 + 16 * (x % 8 ^ turn);
-      i32x4* at = lds + at_stage + x;
+#pragma unroll
+    for (int i = 0; i < LA + LB; i++) {
+      const uint32_t r = ((i < LA ? i : i - LA) * T + t) / 8;
+      const uint32_t k = k0 + 16 * (t % 8 ^ (i < LA ? r & 7 : (r & 3) | (r >> 3 & 1) << 2));
+      i32x4* at = lds + at_stage + i * T + t;
       if (k + 16 > g.K) *at = cut(*at, k, g.K);
     }
-    __syncthreads();
   };
-  // waits for all but this wave's youngest loads and its LDS reads, then everyone's
-  constexpr int kYoung = (S - 2) * (LA + LB);
-  static_assert(kYoung + LA + LB < 64, "s_waitcnt counts to 63");
+  // waits for all but this wave's youngest `left` loads
   const auto arrived = [](auto left) {
     constexpr int n = decltype(left)::value;
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((n & 15) | (n >> 4) << 14 | 0x0070);
+    __builtin_amdgcn_s_waitcnt((n & 15) | (n >> 4) << 14 | 0x0f70);
+    asm volatile("" ::: "memory");
+  };
+  // for everyone, with this wave's LDS reads and writes done
+  const auto together = [] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xc07f);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
+  constexpr int L = LA + LB, kYoung = (S - 2) * L, kEarly = LA + LB / 2;
+  static_assert(kYoung + L < 64, "s_waitcnt counts to 63");
 
   const uint32_t p = lane % 16, q = lane / 16;
   const uint32_t wm = wave % WM * (BM / WM), wn = wave / WM * (BN / WN);
   const uint32_t at = q ^ (lane & 7);
   uint32_t xa = (wm + p) * 8 + at, xb = BM * 8 + (wn + p / 4 * 8 + p % 4) * 8 + at;
+  constexpr int kHeld = Turns ? FN / 2 : 2;  // columns whose codes are held
   f32x4 acc[FM][FN] = {};
-  i32x4 fa[FM][2], fb[2][2];
-  float s[FM], sa[FM];
+  i32x4 fa[FM][2], fb[kHeld][2];
+  float s[FM] = {}, sa[FM];
   const auto read_a = [&](int i) {
 #pragma unroll
     for (int h = 0; h < 2; h++) fa[i][h] = lds[(xa ^ (4 * h)) + i * 128];
   };
   const auto read_b = [&](int j) {
 #pragma unroll
-    for (int h = 0; h < 2; h++) fb[j % 2][h] = lds[(xb ^ (4 * h)) + (j / 2 * 32 + j % 2 * 4) * 8];
+    for (int h = 0; h < 2; h++) fb[j % kHeld][h] = lds[(xb ^ (4 * h)) + (j / 2 * 32 + j % 2 * 4) * 8];
   };
   // the tokens' scales of a block
   const auto read_scales = [&](uint32_t step) {
@@ -252,8 +263,15 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_tile_f8(F8Args g, Grid gr) 
 #pragma unroll
     for (int i = 0; i < FM; i++) sa[i] = from[i * 16 * kChunk];
   };
+  // The weights' scales of this wave's channels, 64 blocks at a time: a word a
+  // lane, in a place of the wave's own.
   const uint32_t nb = (n0 + wn < g.N ? n0 + wn : g.N - 1) / 128;
-  const ConstF sbp = constant(job.sb + (size_t)nb * g.ldsb);
+  const i32x4 rsb = buffer_at(job.sb + (size_t)nb * g.ldsb);
+  const auto load_sb = [&](uint32_t from) {
+    const uint32_t at = from + lane < steps ? from + lane : steps - 1;
+    load_word_to_lds(rsb, lds_at(lsb) + (from / 64 & 1) * (T * 4) + wave * 256, 4 * at, 0);
+  };
+  const auto read_sb = [&](uint32_t step) { return lsb[step / 64 & 1][wave * 64 + step % 64]; };
 
   // the bias, for the end
   const uint16_t* bias = reinterpret_cast<const uint16_t*>(job.bias);
@@ -265,77 +283,177 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void k_tile_f8(F8Args g, Grid gr) 
   const i32x4 rs = buffer_at(g.sa + from * g.ldsa);
   load_scales(rs, 0);
   load_scales(rs, 1);
+  load_sb(0);
+  load_sb(64);
   offsets(0);
 #pragma unroll
-  for (uint32_t s = 0; s < S; s++) {
+  for (uint32_t s = 0; s < (Turns ? S : S - 1); s++) {
     if (s + 1 == steps && cut_last) offsets(s * kStep);
     end_buffer(ra, s, steps);
     end_buffer(rb, s, steps);
 #pragma unroll
-    for (int i = 0; i < LA + LB; i++) load(i, ra, rb, s < steps ? s * kStep : 0u, s * kStage * 16);
+    for (int i = 0; i < L; i++)
+      if (!Turns || s == 0 || i < LA || (i - LA) % 2 == 0)
+        load(i, ra, rb, s < steps ? s * kStep : 0u, s * kStage * 16);
   }
-  float sb = sbp[0];
-  arrived(std::integral_constant<int, kYoung + LA + LB>{});
+  arrived(std::integral_constant<int, Turns ? kEarly : kYoung>{});
   if (steps == 1 && cut_last) cut_stage(0);
-  read_b(0);
-#pragma unroll
-  for (int i = 0; i < FM; i++) read_a(i);
-  read_scales(0);
+  together();
 
-  // One stage a turn: FN columns of FM products, the results of one joined to
-  // the sums while the next ones run, the next column's codes read meanwhile.
-  // Before the last column the next stage has arrived and everyone has read this
-  // one: then the next one's first codes are read, each over the one just used,
-  // and the stage S after this one is loaded over it, over the next columns.
   constexpr int kProducts = FM * FN, kLag = 2;
-  f32x4 d[4];
+  f32x4 d[4] = {};
+  // the x-th product of a stage, and the one before the last added to its sum
+  const auto multiply = [&](int x) {
+    d[x % 4] = block_sum(fb[x / FM % kHeld], fa[x % FM]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const auto add = [&](int x) {
+    add_scaled(acc[x % FM][x / FM], d[x % 4], s[x % FM]);
+    here(acc[x % FM][x / FM]);
+  };
   uint32_t to = 0;                           // this stage's place, in pieces
-  uint32_t old_to = 0;
-  for (uint32_t step = 0; step < steps; step++) {
+  if constexpr (Turns) {
+    // The two waves of a SIMD take turns: while one multiplies half a stage, the
+    // other reads the codes of its own next half.  Waves 4 to 7 are one turn
+    // behind: counting from the first waves' first reads of a stage, it is read
+    // in turns 0 to 3, all of a and the first half of b (kEarly loads: of every
+    // 128 channels the first 64) in turns 0 and 1.  The stage after the next is
+    // loaded over it between the products of turns 2 and 3, the second half of b
+    // in turns 4 and 5, and has arrived at the end of turn 7.
+    const auto run = [&](auto late) {
+      const auto load_half = [&](int n, uint32_t stage) {      // the n-th load
+        const int i = n < LA ? n : n < kEarly ? LA + 2 * (n - LA) : LA + 1 + 2 * (n - kEarly);
+        load(i, ra, rb, stage < steps ? stage * kStep : 0u, stage % 2 * kStage * 16);
+      };
+      const auto aim = [&](uint32_t stage) {
+        if (stage + 1 == steps && cut_last) offsets(stage * kStep);
+        end_buffer(ra, stage, steps);
+        end_buffer(rb, stage, steps);
+      };
+      const auto stage_arrived = [&](uint32_t stage) {
+        arrived(std::integral_constant<int, kEarly>{});
+        if (stage + 1 == steps && cut_last) cut_stage(stage % 2 * kStage);
+      };
+      // half a stage's products, and loads n0 to n1 of `stage` between them
+      const auto turn = [&](int half, int n0, int n1, uint32_t stage) {
+        aim(stage);
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int i = 0; i < FM; i++) s[i] = sa[i] * sb;
-    const uint32_t next = to == (S - 1) * kStage ? 0 : to + kStage;
+        for (int y = 0; y < kProducts / 2; y++) {
+          const int x = half * (kProducts / 2) + y;
+          __builtin_amdgcn_sched_barrier(0);
+          multiply(x);
+          if (y % 2 == 1 && n0 + y / 2 < n1) load_half(n0 + y / 2, stage);
+          if (y >= kLag) add(x - kLag);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        __builtin_amdgcn_s_setprio(0);
+      };
+      if (late) together();
+#pragma unroll 1
+      for (uint32_t step = 0; step < steps; step++) {
+        const float sb = read_sb(step);
 #pragma unroll
-    for (int j = 0; j < FN; j++) {
-      if (j + 1 < FN) read_b(j + 1);
-      if (j + 2 == FN) {
-        const uint32_t after = step + 1 < steps ? step + 1 : step;
-        read_scales(after);
-        sb = sbp[after];
-      }
-      if (j + 1 == FN) {
-        arrived(std::integral_constant<int, kYoung>{});
-        if (step + 2 == steps && cut_last) cut_stage(next);
-        if (step + 1 + S == steps && cut_last) offsets((step + S) * kStep);
-        end_buffer(ra, step + S, steps);
-        end_buffer(rb, step + S, steps);
-        xa += next - to;
-        xb += next - to;
-        old_to = to;
+        for (int j = 0; j < FN / 2; j++) read_b(j);
+#pragma unroll
+        for (int i = 0; i < FM; i++) read_a(i);
+        read_scales(step);
+#pragma unroll
+        for (int x = kProducts - kLag; x < kProducts; x++) add(x);
+        together();
+#pragma unroll
+        for (int i = 0; i < FM; i++) s[i] = sa[i] * sb;
+        if (late) turn(0, 0, kEarly, step + 2);
+        else turn(0, kEarly, L, step + 1);
+        together();
+#pragma unroll
+        for (int j = FN / 2; j < FN; j++) read_b(j);
+#pragma unroll
+        for (int x = kProducts / 2 - kLag; x < kProducts / 2; x++) add(x);
+        if (late) stage_arrived(step + 1);
         if ((step + 1) % kChunk == 0) load_scales(rs, step / kChunk + 2);
+        if (step % 64 == 63) load_sb(step + 65);
+        xa += kStage - 2 * to;
+        xb += kStage - 2 * to;
+        to = kStage - to;
+        together();
+        if (late) turn(1, kEarly, L, step + 2);
+        else turn(1, 0, kEarly, step + 2);
+        if (!late) stage_arrived(step + 1);
+        together();
       }
 #pragma unroll
-      for (int i = 0; i < FM; i++) {
-        const int x = j * FM + i;
-        __builtin_amdgcn_sched_barrier(0);
-        d[x % 4] = block_sum(fb[j % 2], fa[i]);
-        if (j + 1 == FN) {
-          if (i == 0) read_b(0);
-          read_a(i);
-        }
-        if (x >= kLag) {
-          const int y = x - kLag;
-          add_scaled(acc[y % FM][y / FM], d[y % 4], s[y % FM]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
+      for (int x = kProducts - kLag; x < kProducts; x++) add(x);
+      if (!late) together();
+    };
+    if (wave < WM * WN / 2) {
+      run(std::false_type{});
+    } else {
+#pragma unroll
+      for (int n = kEarly; n < L; n++)       // of stage 1
+        load(LA + 1 + 2 * (n - kEarly), ra, rb, steps > 1 ? kStep : 0u, kStage * 16);
+      run(std::true_type{});
     }
+  } else {
+    // FN columns of FM products a stage, the results of one joined to the sums
+    // while the next ones run, the next column's codes read meanwhile.  Before the
+    // last column the next stage has arrived and everyone has read this one: then
+    // the next one's first codes are read, each over the one just used.  Over the
+    // place of the stage before this one the stage S - 1 after this one is loaded.
+    constexpr int kLoads = (L + FM * (FN - 1) - 1) / (FM * (FN - 1));   // a product
+    float sb = read_sb(0);
+    uint32_t free = (S - 1) * kStage;        // the place to load, in pieces
+    read_b(0);
 #pragma unroll
-    for (int y = kProducts - kLag; y < kProducts; y++) add_scaled(acc[y % FM][y / FM], d[y % 4], s[y % FM]);
+    for (int i = 0; i < FM; i++) read_a(i);
+    read_scales(0);
+    for (uint32_t step = 0; step < steps; step++) {
 #pragma unroll
-    for (int i = 0; i < LA + LB; i++)
-      load(i, ra, rb, step + S < steps ? (step + S) * kStep : 0u, old_to * 16);
-    to = next;
+      for (int i = 0; i < FM; i++) s[i] = sa[i] * sb;
+      const uint32_t next = to == (S - 1) * kStage ? 0 : to + kStage, coming = step + S - 1;
+      if (coming + 1 == steps && cut_last) offsets(coming * kStep);
+      end_buffer(ra, coming, steps);
+      end_buffer(rb, coming, steps);
+      const uint32_t k = coming < steps ? coming * kStep : 0u;
+#pragma unroll
+      for (int j = 0; j < FN; j++) {
+        if (j + 1 < FN) read_b(j + 1);
+        if (j + 2 == FN) {
+          const uint32_t after = step + 1 < steps ? step + 1 : step;
+          read_scales(after);
+          sb = read_sb(after);
+        }
+        if (j + 1 == FN) {
+          arrived(std::integral_constant<int, kYoung>{});
+          if (step + 2 == steps && cut_last) cut_stage(next);
+          together();
+          xa += next - to;
+          xb += next - to;
+        }
+#pragma unroll
+        for (int i = 0; i < FM; i++) {
+          const int x = j * FM + i;
+          __builtin_amdgcn_sched_barrier(0);
+          multiply(x);
+          if (j + 1 == FN) {
+            if (i == 0) read_b(0);
+            read_a(i);
+          } else {
+#pragma unroll
+            for (int r = x * kLoads; r < (x + 1) * kLoads; r++)
+              if (r < L) load(r, ra, rb, k, free * 16);
+          }
+          if (x >= kLag) add(x - kLag);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      if ((step + 1) % kChunk == 0) load_scales(rs, step / kChunk + 2);
+      if (step % 64 == 63) load_sb(step + 65);
+#pragma unroll
+      for (int x = kProducts - kLag; x < kProducts; x++) add(x);
+      free = to;
+      to = next;
+    }
   }
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt(0x0f70);        // nothing may still be on its way to LDS
