@@ -15,33 +15,39 @@ typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 // assembly since the compiler, where it cannot tell two LDS buffers apart,
 // would wait for the load before any LDS read: the caller waits.  It has no
 // output register, so nothing is written behind the compiler's back but LDS:
-// m0, which holds the LDS address, is an input that the compiler sets (the wait
-// state is the one that a load through m0 needs after that).
+// m0, which holds the LDS address, is an input that the compiler sets.  The wait
+// states are those that a memory instruction needs after a vector instruction
+// wrote its scalar operands: the compiler, which does not see the load, may restore
+// spilled ones (v_readlane_b32) right before the statement.
+// The buffer must be in scalar registers when it gets here: one that the compiler
+// holds in vector registers, because it cannot tell that all lanes hold the same
+// (see uniform), would be misread.
 // Once: past the caches, for what no other workgroup reads.
 template <bool Once>
 __device__ __forceinline__ void load_to_lds(i32x4 rsrc, uint32_t lds, uint32_t voff,
                                             uint32_t soff) {
   if constexpr (Once)
-    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
                  :
                  : "{m0}"(lds), "v"(voff), "s"(rsrc), "s"(soff)
                  : "memory");
   else
-    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
                  : "{m0}"(lds), "v"(voff), "s"(rsrc), "s"(soff)
                  : "memory");
 }
-// A buffer that starts at p, for load_to_lds.  The wait states are those that
-// a memory instruction needs after a vector instruction (readfirstlane) wrote
-// its scalar operands: the compiler does not see the loads in the assembly.
-// Later changes of a buffer are scalar instructions, which need none.
+// A buffer that starts at p, for load_to_lds.
 __device__ __forceinline__ i32x4 buffer_at(const void* p) {
   const uint64_t a = (uint64_t)p;
   const int lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
   const int hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)) & 0xffff;
-  i32x4 r = {lo, hi, -1, 0x00027000};
-  asm volatile("s_nop 4" : "+s"(r));
+  return i32x4{lo, hi, -1, 0x00027000};
+}
+// the same buffer, of which the compiler knows that all lanes hold the same
+__device__ __forceinline__ i32x4 uniform(i32x4 r) {
+#pragma unroll
+  for (int i = 0; i < 4; i++) r[i] = __builtin_amdgcn_readfirstlane(r[i]);
   return r;
 }
 // all of the buffer while s < steps, afterwards nothing (and nothing is fetched)

@@ -29,7 +29,7 @@ typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 // 4 bytes a lane, as load_to_lds
 __device__ __forceinline__ void load_word_to_lds(i32x4 rsrc, uint32_t lds, uint32_t voff,
                                                  uint32_t soff) {
-  asm volatile("s_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+  asm volatile("s_nop 4\n\tbuffer_load_dword %1, %2, %3 offen lds"
                :
                : "{m0}"(lds), "v"(voff), "s"(rsrc), "s"(soff)
                : "memory");
@@ -314,86 +314,80 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile_f8(F8Args g, Grid gr) 
   uint32_t to = 0;                           // this stage's place, in pieces
   if constexpr (Turns) {
     // The two waves of a SIMD take turns: while one multiplies half a stage, the
-    // other reads the codes of its own next half.  Waves 4 to 7 are one turn
-    // behind: counting from the first waves' first reads of a stage, it is read
-    // in turns 0 to 3, all of a and the first half of b (kEarly loads: of every
-    // 128 channels the first 64) in turns 0 and 1.  The stage after the next is
-    // loaded over it between the products of turns 2 and 3, the second half of b
-    // in turns 4 and 5, and has arrived at the end of turn 7.
-    const auto run = [&](auto late) {
-      const auto load_half = [&](int n, uint32_t stage) {      // the n-th load
+    // other reads the codes of its own next half and issues its loads, which would
+    // hold up the products (a turn of 16 products took 790 cycles with two loads
+    // among them, 940 with six, and takes 540 by itself).  Waves 4 to 7 are one turn
+    // behind: counting from the first waves' first reads of a stage, it is read in
+    // turns 0 to 3, all of a and the first half of b (kEarly loads: of every 128
+    // channels the first 64) in turns 0 and 1.  Over these the stage after the next
+    // is loaded in turns 2 and 3, over the second half of b in turns 4 and 5; it has
+    // arrived at the end of turn 7.
+    const bool late = wave >= WM * WN / 2;
+    // loads n0 to n1 of `stage`
+    const auto load_part = [&](int n0, int n1, uint32_t stage) {
+      if (n0 == 0 && stage + 1 == steps && cut_last) offsets(stage * kStep);
+      end_buffer(ra, stage, steps);
+      end_buffer(rb, stage, steps);
+#pragma unroll
+      for (int n = n0; n < n1; n++) {
         const int i = n < LA ? n : n < kEarly ? LA + 2 * (n - LA) : LA + 1 + 2 * (n - kEarly);
         load(i, ra, rb, stage < steps ? stage * kStep : 0u, stage % 2 * kStage * 16);
-      };
-      const auto aim = [&](uint32_t stage) {
-        if (stage + 1 == steps && cut_last) offsets(stage * kStep);
-        end_buffer(ra, stage, steps);
-        end_buffer(rb, stage, steps);
-      };
-      const auto stage_arrived = [&](uint32_t stage) {
-        arrived(std::integral_constant<int, kEarly>{});
-        if (stage + 1 == steps && cut_last) cut_stage(stage % 2 * kStage);
-      };
-      // half a stage's products, and loads n0 to n1 of `stage` between them
-      const auto turn = [&](int half, int n0, int n1, uint32_t stage) {
-        aim(stage);
-        __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-        for (int y = 0; y < kProducts / 2; y++) {
-          const int x = half * (kProducts / 2) + y;
-          __builtin_amdgcn_sched_barrier(0);
-          multiply(x);
-          if (y % 2 == 1 && n0 + y / 2 < n1) load_half(n0 + y / 2, stage);
-          if (y >= kLag) add(x - kLag);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        __builtin_amdgcn_s_setprio(0);
-      };
-      if (late) together();
-#pragma unroll 1
-      for (uint32_t step = 0; step < steps; step++) {
-        const float sb = read_sb(step);
-#pragma unroll
-        for (int j = 0; j < FN / 2; j++) read_b(j);
-#pragma unroll
-        for (int i = 0; i < FM; i++) read_a(i);
-        read_scales(step);
-#pragma unroll
-        for (int x = kProducts - kLag; x < kProducts; x++) add(x);
-        together();
-#pragma unroll
-        for (int i = 0; i < FM; i++) s[i] = sa[i] * sb;
-        if (late) turn(0, 0, kEarly, step + 2);
-        else turn(0, kEarly, L, step + 1);
-        together();
-#pragma unroll
-        for (int j = FN / 2; j < FN; j++) read_b(j);
-#pragma unroll
-        for (int x = kProducts / 2 - kLag; x < kProducts / 2; x++) add(x);
-        if (late) stage_arrived(step + 1);
-        if ((step + 1) % kChunk == 0) load_scales(rs, step / kChunk + 2);
-        if (step % 64 == 63) load_sb(step + 65);
-        xa += kStage - 2 * to;
-        xb += kStage - 2 * to;
-        to = kStage - to;
-        together();
-        if (late) turn(1, kEarly, L, step + 2);
-        else turn(1, 0, kEarly, step + 2);
-        if (!late) stage_arrived(step + 1);
-        together();
       }
+    };
+    const auto stage_arrived = [&](uint32_t stage) {
+      arrived(std::integral_constant<int, kEarly>{});
+      if (stage + 1 == steps && cut_last) cut_stage(stage % 2 * kStage);
+    };
+    const auto turn = [&](int half) {
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int y = 0; y < kProducts / 2; y++) {
+        const int x = half * (kProducts / 2) + y;
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(x);
+        if (y >= kLag) add(x - kLag);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      __builtin_amdgcn_s_setprio(0);
+    };
+    if (late) together();
+#pragma unroll 1
+    for (uint32_t step = 0; step < steps; step++) {
+      const float sb = read_sb(step);
+#pragma unroll
+      for (int j = 0; j < FN / 2; j++) read_b(j);
+#pragma unroll
+      for (int i = 0; i < FM; i++) read_a(i);
+      read_scales(step);
+      __builtin_amdgcn_sched_barrier(0);
+      load_part(kEarly, L, step + 1);
 #pragma unroll
       for (int x = kProducts - kLag; x < kProducts; x++) add(x);
-      if (!late) together();
-    };
-    if (wave < WM * WN / 2) {
-      run(std::false_type{});
-    } else {
+      together();
 #pragma unroll
-      for (int n = kEarly; n < L; n++)       // of stage 1
-        load(LA + 1 + 2 * (n - kEarly), ra, rb, steps > 1 ? kStep : 0u, kStage * 16);
-      run(std::true_type{});
+      for (int i = 0; i < FM; i++) s[i] = sa[i] * sb;
+      turn(0);
+      together();
+#pragma unroll
+      for (int j = FN / 2; j < FN; j++) read_b(j);
+      __builtin_amdgcn_sched_barrier(0);
+      load_part(0, kEarly, step + 2);
+#pragma unroll
+      for (int x = kProducts / 2 - kLag; x < kProducts / 2; x++) add(x);
+      if (late) stage_arrived(step + 1);
+      xa += kStage - 2 * to;
+      xb += kStage - 2 * to;
+      to = kStage - to;
+      together();
+      turn(1);
+      if (!late) stage_arrived(step + 1);
+      if ((step + 1) % kChunk == 0) load_scales(rs, step / kChunk + 2);
+      if (step % 64 == 63) load_sb(step + 65);
+      together();
     }
+#pragma unroll
+    for (int x = kProducts - kLag; x < kProducts; x++) add(x);
+    if (!late) together();
   } else {
     // FN columns of FM products a stage, the results of one joined to the sums
     // while the next ones run, the next column's codes read meanwhile.  Before the

@@ -320,7 +320,9 @@ def check_product(c, want, tol, label):
 SIZES = [(1, 16, 16), (1, 1, 1), (3, 5, 7), (1, 300, 16384), (1, 1000, 1000), (7, 130, 129), (8, 4112, 300),
          (9, 257, 255), (16, 2048, 1024), (17, 100, 4096), (33, 500, 640), (48, 1000, 130), (64, 64, 2000),
          (64, 4096, 512), (100, 333, 1025), (128, 128, 128), (130, 300, 257), (200, 5003, 520), (333, 1003, 2050),
-         (512, 2048, 384), (1024, 1024, 256), (1000, 3000, 300), (2048, 4096, 144), (2050, 4100, 272)]
+         (512, 2048, 384), (1024, 1024, 256), (1000, 3000, 300), (2048, 4096, 144), (2050, 4100, 272),
+         # more tiles than workgroups, and scales that come in several parts
+         (4100, 4200, 1100), (3000, 8200, 2100)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
@@ -405,7 +407,7 @@ def sizes_of_groups(kind, E, M, g):
 
 GROUPED = [(1, 1, 64, 128), (4, 3, 100, 200), (8, 40, 256, 512), (3, 700, 300, 260), (32, 64, 512, 1024),
            (130, 300, 200, 144), (64, 1000, 130, 300), (5, 3000, 520, 129), (300, 2000, 64, 128), (8, 4096, 1024, 256),
-           (1024, 50, 48, 48), (7, 9000, 256, 384)]
+           (1024, 50, 48, 48), (7, 9000, 256, 384), (8, 6000, 4096, 1040), (70, 9000, 2100, 1152)]
 
 
 @pytest.mark.parametrize("kind", ["even", "one", "short", "random"])
