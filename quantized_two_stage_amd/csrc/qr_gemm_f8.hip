@@ -170,8 +170,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile_f8(F8Args g, Grid gr) 
   if (!find_job<BM, BN, Grouped>(g, gr, job)) return;
   const uint32_t m0 = job.m0, n0 = job.n0;
   const uint32_t K16 = (g.K + 15) & ~15u;
-  const uint32_t steps = (g.K + kStep - 1) / kStep;
-  const bool cut_last = g.K % kStep != 0;
+  const uint32_t steps = (g.K + kF8Step - 1) / kF8Step;
+  const bool cut_last = g.K % kF8Step != 0;
 
   // offsets of this lane's pieces in the stage at k; rows past the last one are
   // read as the last one, pieces past a row's end as its last
@@ -214,7 +214,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile_f8(F8Args g, Grid gr) 
   // zeros for the codes of the last stage that lie past K, of a and b: either may
   // hold NaN codes there.  Every lane's own pieces, once they have arrived.
   const auto cut_stage = [&](uint32_t at_stage) {
-    const uint32_t k0 = (steps - 1) * kStep;
+    const uint32_t k0 = (steps - 1) * kF8Step;
 #pragma unroll
     for (int i = 0; i < LA + LB; i++) {
       const uint32_t r = ((i < LA ? i : i - LA) * T + t) / 8;
@@ -288,13 +288,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile_f8(F8Args g, Grid gr) 
   offsets(0);
 #pragma unroll
   for (uint32_t s = 0; s < (Turns ? S : S - 1); s++) {
-    if (s + 1 == steps && cut_last) offsets(s * kStep);
+    if (s + 1 == steps && cut_last) offsets(s * kF8Step);
     end_buffer(ra, s, steps);
     end_buffer(rb, s, steps);
 #pragma unroll
     for (int i = 0; i < L; i++)
       if (!Turns || s == 0 || i < LA || (i - LA) % 2 == 0)
-        load(i, ra, rb, s < steps ? s * kStep : 0u, s * kStage * 16);
+        load(i, ra, rb, s < steps ? s * kF8Step : 0u, s * kStage * 16);
   }
   arrived(std::integral_constant<int, Turns ? kEarly : kYoung>{});
   if (steps == 1 && cut_last) cut_stage(0);
@@ -325,13 +325,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile_f8(F8Args g, Grid gr) 
     const bool late = wave >= WM * WN / 2;
     // loads n0 to n1 of `stage`
     const auto load_part = [&](int n0, int n1, uint32_t stage) {
-      if (n0 == 0 && stage + 1 == steps && cut_last) offsets(stage * kStep);
+      if (n0 == 0 && stage + 1 == steps && cut_last) offsets(stage * kF8Step);
       end_buffer(ra, stage, steps);
       end_buffer(rb, stage, steps);
 #pragma unroll
       for (int n = n0; n < n1; n++) {
         const int i = n < LA ? n : n < kEarly ? LA + 2 * (n - LA) : LA + 1 + 2 * (n - kEarly);
-        load(i, ra, rb, stage < steps ? stage * kStep : 0u, stage % 2 * kStage * 16);
+        load(i, ra, rb, stage < steps ? stage * kF8Step : 0u, stage % 2 * kStage * 16);
       }
     };
     const auto stage_arrived = [&](uint32_t stage) {
@@ -405,10 +405,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile_f8(F8Args g, Grid gr) 
 #pragma unroll
       for (int i = 0; i < FM; i++) s[i] = sa[i] * sb;
       const uint32_t next = to == (S - 1) * kStage ? 0 : to + kStage, coming = step + S - 1;
-      if (coming + 1 == steps && cut_last) offsets(coming * kStep);
+      if (coming + 1 == steps && cut_last) offsets(coming * kF8Step);
       end_buffer(ra, coming, steps);
       end_buffer(rb, coming, steps);
-      const uint32_t k = coming < steps ? coming * kStep : 0u;
+      const uint32_t k = coming < steps ? coming * kF8Step : 0u;
 #pragma unroll
       for (int j = 0; j < FN; j++) {
         if (j + 1 < FN) read_b(j + 1);
@@ -492,8 +492,8 @@ __global__ __launch_bounds__(64 * W) void k_split_f8(F8Args g, Grid gr) {
   if (!find_job<BM, BN, Grouped>(g, gr, job)) return;
   const uint32_t n0 = job.n0;
   const uint32_t K16 = (g.K + 15) & ~15u;
-  const uint32_t steps = (g.K + kStep - 1) / kStep;
-  const bool cut_last = g.K % kStep != 0;
+  const uint32_t steps = (g.K + kF8Step - 1) / kF8Step;
+  const bool cut_last = g.K % kF8Step != 0;
   uint32_t ra0[LA], va[LA], vb[LB];
 #pragma unroll
   for (int i = 0; i < LA; i++) ra0[i] = row_of<Grouped>(g, job, i * 8 + lane / 8) * (uint32_t)g.lda;
@@ -524,7 +524,7 @@ __global__ __launch_bounds__(64 * W) void k_split_f8(F8Args g, Grid gr) {
     return s + 1 >= steps ? (s < steps ? s : 0u) : at;
   };
   const auto load = [&](uint32_t s, uint32_t to) {
-    const uint32_t at = block_of(s), k = at * kStep;
+    const uint32_t at = block_of(s), k = at * kF8Step;
     end_buffer(ra, s, steps);
     end_buffer(rb, s, steps);
     end_buffer(rs, s, steps);
@@ -554,7 +554,7 @@ __global__ __launch_bounds__(64 * W) void k_split_f8(F8Args g, Grid gr) {
     i32x4* const at = ring + to * kStage;
     if (s + 1 == steps && cut_last) {
       // zeros for the codes past K, of a and b: either may hold NaN codes there
-      const uint32_t k = s * kStep + 16 * (lane % 8 ^ lane / 8);
+      const uint32_t k = s * kF8Step + 16 * (lane % 8 ^ lane / 8);
 #pragma unroll
       for (int i = 0; i < LA + LB; i++)
         if (k + 16 > g.K) at[i * 64 + lane] = cut(at[i * 64 + lane], k, g.K);
@@ -621,7 +621,7 @@ __global__ __launch_bounds__(64 * W) void k_split_f8(F8Args g, Grid gr) {
 
 template <int I>
 hipError_t launch_tile(int dtype, const F8Args& g, hipStream_t st) {
-  constexpr Tile t = kF8Tiles[I];
+  constexpr F8Tile t = kF8Tiles[I];
   const Grid gr{f8_tile_rows(t.bm, g.M, g.E), (g.N + t.bn - 1) / t.bn, t.group};
   const dim3 grid(gr.tm * gr.tn), block(64 * t.wm * (t.wn ? t.wn : 1));
   const auto kernel = [&](auto d, auto once, auto grouped) {
@@ -631,12 +631,13 @@ hipError_t launch_tile(int dtype, const F8Args& g, hipStream_t st) {
     else k_tile_f8<t.bm, t.bn, t.wm, t.wn, t.stages, D, Once, Grouped><<<grid, block, 0, st>>>(g, gr);
   };
   const auto of_type = [&](auto d) {
+    const bool once = f8_weights_once(t.bm, g.M, g.E);
     if (g.E == 0) {
-      if constexpr (t.bm <= 8) kernel(d, std::true_type{}, std::false_type{});   // never more tokens
-      else if (gr.tm == 1) kernel(d, std::true_type{}, std::false_type{});
+      if (once) kernel(d, std::true_type{}, std::false_type{});
       else kernel(d, std::false_type{}, std::false_type{});
     } else {
-      kernel(d, std::false_type{}, std::true_type{});
+      if (once) kernel(d, std::true_type{}, std::true_type{});
+      else kernel(d, std::false_type{}, std::true_type{});
     }
   };
   if (dtype == kF16) of_type(std::integral_constant<int, kF16>{});

@@ -3,31 +3,43 @@
 // the tests that run every tile.  Not part of the ABI.
 #pragma once
 
+#include <cmath>
 #include <stddef.h>
 #include <stdint.h>
 
-#include "qr_gemm_tiles.h"
-
 namespace qr {
 
-// As kTiles: what a workgroup takes to start and end, and for each block of 128
-// of the sum, ns, where every CU has one at most.
-constexpr Tile kF8Tiles[] = {
-    {8, 16, 8, 0, 2, 1, 0, 0},
-    {8, 16, 4, 0, 3, 1, 0, 0},
-    {16, 16, 8, 0, 2, 16, 2800, 65},
-    {16, 32, 4, 0, 3, 16, 2900, 100},
-    {32, 32, 4, 0, 2, 16, 3100, 130},
-    {64, 32, 4, 0, 3, 16, 4000, 190},
-    {64, 64, 4, 0, 2, 16, 4500, 240},
-    {64, 64, 2, 2, 4, 8, 3000, 290},
-    {64, 128, 2, 4, 5, 8, 3400, 360},
-    {128, 64, 4, 2, 5, 8, 3400, 380},
-    {128, 128, 2, 4, 4, 8, 4000, 520},
-    {128, 256, 2, 4, 3, 8, 4500, 780},
-    {256, 256, 4, 2, 2, 4, 5500, 1350},
+// Tiles, and what they were measured to take, in ns.  Their workgroups come in
+// rounds of `at_once` on each of 256 CUs; a round takes `start` and `stage` for
+// each block of 128 of the sum.  Where there are many, a CU takes `more` and
+// `full` a block for each workgroup.  The weights' bytes take their time beside
+// that (6000 a ns where they are read once, else 5300): of the shorter of the two
+// `once` or `again` percent are added.
+// Fitted to the times of all tiles at 320 sizes (1 to 8192 tokens, sums and
+// channels of 64 to 16384, one product or 4 to 128 experts, cold weights); the
+// tile estimated to end first against the fastest at each: 1.00 at the median,
+// within 1.13 at nine of ten, 1.31 at worst (20 experts, 20 rows, 1664 x 640).
+struct F8Tile {
+  uint32_t bm, bn;                    // tokens and channels
+  uint32_t wm, wn;                    // waves; wn == 0: wm waves that share the sum
+  uint32_t stages;                    // of a ring
+  uint32_t group;                     // tile rows that neighbouring workgroups share
+  uint32_t at_once, start, stage, more, full, once, again;
+};
+constexpr F8Tile kF8Tiles[] = {
+    {8, 16, 4, 0, 3, 1, 3, 3150, 59, 680, 31, 54, 77},
+    {16, 16, 8, 0, 2, 16, 2, 3270, 56, 1460, 31, 64, 90},
+    {16, 32, 4, 0, 3, 16, 2, 3220, 103, 2010, 43, 64, 82},
+    {32, 32, 4, 0, 2, 16, 2, 3310, 160, 3050, 28, 51, 70},
+    {64, 64, 2, 2, 4, 8, 2, 4050, 406, 2080, 246, 38, 81},
+    {64, 128, 2, 4, 5, 8, 1, 4660, 446, 730, 686, 24, 42},
+    {128, 64, 4, 2, 5, 8, 1, 4370, 467, 4290, 492, 30, 83},
+    {128, 128, 2, 4, 4, 8, 1, 5180, 582, 4380, 822, 30, 116},
+    {128, 256, 2, 4, 3, 8, 1, 6090, 848, 2820, 1508, 40, 120},
+    {256, 256, 4, 2, 2, 4, 1, 8240, 1208, 12040, 1268, 28, 25},
 };
 constexpr int kF8TileCount = sizeof(kF8Tiles) / sizeof(kF8Tiles[0]);
+constexpr uint32_t kF8Step = 128;     // codes of a block
 
 // Rows of tiles of `bm` rows that M rows of E experts fill at most (E == 0: one
 // product), whatever their offsets: every expert with rows may end in a short
@@ -39,22 +51,41 @@ constexpr uint32_t f8_tile_rows(uint32_t bm, uint32_t M, uint32_t E) {
 // about as many as there will be: half a tile of each expert stays empty
 constexpr uint32_t f8_tile_rows_likely(uint32_t bm, uint32_t M, uint32_t E) {
   const uint32_t most = f8_tile_rows(bm, M, E), some = E < M ? E : M;
-  const uint32_t likely = E == 0 ? most : M / bm + (some + 1) / 2;
+  const uint32_t likely = M / bm + (some + 1) / 2;
   return E == 0 ? most : likely < some ? some : likely < most ? likely : most;
+}
+
+// Whether most weights are read by one workgroup alone, and go past the caches:
+// one row of tiles, or experts of half a tile's rows on average.  Weights of 32
+// experts, 2048 x 8192, us: 64 rows in tiles of 8 69 (through the caches 77), of 16
+// 82 (90); 2048 x 4096: 256 rows in tiles of 16 53 (57), 512 rows in tiles of 32 61
+// (64), but in tiles of 16 74 (67).
+constexpr bool f8_weights_once(uint32_t bm, uint32_t M, uint32_t E) {
+  return E == 0 ? M <= bm : 2 * (uint64_t)M <= (uint64_t)bm * (E < M ? E : M);
+}
+
+inline double f8_estimate(const F8Tile& t, uint32_t M, uint32_t N, uint32_t K, uint32_t E) {
+  const uint32_t steps = (K + kF8Step - 1) / kF8Step;
+  const double blocks = (double)f8_tile_rows_likely(t.bm, M, E) * ((N + t.bn - 1) / t.bn);
+  const double few = std::ceil(blocks / (256 * t.at_once)) * (t.start + (double)steps * t.stage);
+  const double many = blocks / 256 * (t.more + (double)steps * t.full);
+  const double work = few > many ? few : many;
+  // experts that get a row, were all chosen alike
+  const double hit = E == 0 ? 1 : E * (1 - std::exp(-(double)M / E));
+  const bool once = f8_weights_once(t.bm, M, E);
+  const double weights = hit * N * K / (once ? 6000 : 5300);
+  const double more = 0.01 * (once ? t.once : t.again);
+  return work > weights ? work + weights * more : weights + work * more;
 }
 
 // Index into kF8Tiles.
 inline int choose_f8_tile(uint32_t M, uint32_t N, uint32_t K, uint32_t E) {
-  if (E == 0 && M <= 8) return N <= 16 * 256 && K >= 32 * kStep ? 0 : 1;
-  const uint64_t steps = (K + kStep - 1) / kStep;
+  if (E == 0 && M <= kF8Tiles[0].bm) return 0;
   int best = -1;
-  uint64_t least = ~0ull;
-  for (int i = 2; i < kF8TileCount; i++) {
-    const Tile& t = kF8Tiles[i];
-    const uint64_t tm = f8_tile_rows_likely(t.bm, M, E), blocks = tm * ((N + t.bn - 1) / t.bn);
-    uint64_t ns = (blocks + 255) / 256 * (t.start + steps * t.stage);
-    if (tm == 1) ns -= ns / 10;
-    if (ns < least) {
+  double least = 0;
+  for (int i = E == 0 ? 1 : 0; i < kF8TileCount; i++) {   // tiles of 8 rows: one row of them, or experts
+    const double ns = f8_estimate(kF8Tiles[i], M, N, K, E);
+    if (best < 0 || ns < least) {
       least = ns;
       best = i;
     }
