@@ -129,7 +129,7 @@ int qr_gemm_f8_grouped(qr_dtype dtype, const uint8_t* a, size_t lda, const float
  *   place     T x k int32: the row of token t's j-th expert, as qr_combine takes it
  * E in 1..QR_MAX_EXPERTS, k in 1..min(E, QR_MAX_CHOSEN), T*k at most 2^22.  T == 0
  * writes E + 1 zeros to offsets.  workspace: qr_route_workspace_bytes(T, E, k)
- * bytes of device memory, 4-byte aligned (0: none needed, NULL will do); two
+ * bytes of device memory, 16-byte aligned (0: none needed, NULL will do); two
  * calls that may run at the same time need one each. */
 int qr_route(int dtype, const void* logits, size_t ldl, size_t T, size_t E, size_t k,
              int renormalize, float* weights, int32_t* experts, int32_t* offsets, int32_t* rows,

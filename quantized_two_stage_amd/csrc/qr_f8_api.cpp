@@ -201,7 +201,7 @@ int qr_route(int dtype, const void* logits, size_t ldl, size_t T, size_t E, size
   const Rows rl{"logits", logits, T, E, ldl, elem, elem}, rw{"weights", weights, 1, n, n, 4, 4},
       re{"experts", experts, 1, n, n, 4, 4}, ro{"offsets", offsets, 1, E + 1, E + 1, 4, 4},
       rr{"rows", rows, 1, n, n, 4, 4}, rp{"place", place, 1, n, n, 4, 4},
-      rws{"workspace", workspace, 1, need / 4, need / 4, 4, 4};
+      rws{"workspace", workspace, 1, need, need, 1, 16};
   QR_TRY(check(ro));
   if (T != 0) {
     for (const Rows* r : {&rl, &rw, &re, &rr, &rp}) QR_TRY(check(*r));
@@ -219,7 +219,7 @@ int qr_route(int dtype, const void* logits, size_t ldl, size_t T, size_t E, size
   }
   const qr::RouteArgs a{static_cast<const uint8_t*>(logits), ldl, (uint32_t)T, (uint32_t)E,
                         (uint32_t)k, renormalize != 0, weights, experts, offsets, rows, place,
-                        static_cast<uint32_t*>(workspace)};
+                        static_cast<uint16_t*>(workspace)};
   (void)hipGetLastError();
   return hip_status(qr::launch_route(dtype, a, as_stream(stream)), "route launch");
 }

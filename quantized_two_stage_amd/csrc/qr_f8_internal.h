@@ -53,7 +53,7 @@ struct RouteArgs {
   bool renormalize;
   float* weights;
   int32_t *experts, *offsets, *rows, *place;
-  uint32_t* counts;        // workspace
+  uint16_t* counts;        // workspace
 };
 
 // type of the logits where they are not 16-bit

@@ -298,7 +298,10 @@ def _mat(what, t, rows, cols, dtype, dev):
     if t.dtype is not dtype or t.get_device() != dev or t.shape != (rows, cols):
         _refuse(what, t, dtype, dev,
                 "%s has shape %s: %s expected" % (what, tuple(t.shape), (rows, cols)))
-    return _ld(what, t, rows, cols)
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError("%s: the values of a row are not contiguous" % what)
+    return ld if rows > 1 else cols
 
 
 def _ld(what, t, rows, cols):
