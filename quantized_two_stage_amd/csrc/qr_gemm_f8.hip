@@ -244,24 +244,26 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile_f8(F8Args g, Grid gr) 
   const uint32_t wm = wave % WM * (BM / WM), wn = wave / WM * (BN / WN);
   const uint32_t at = q ^ (lane & 7);
   uint32_t xa = (wm + p) * 8 + at, xb = BM * 8 + (wn + p / 4 * 8 + p % 4) * 8 + at;
-  constexpr int kHeld = Turns ? FN / 2 : 2;  // columns whose codes are held
+  constexpr int kHeld = Turns ? FN / 2 : FN;  // columns whose codes are held
+  constexpr int kSets = Turns ? 1 : 2;
   f32x4 acc[FM][FN] = {};
-  i32x4 fa[FM][2], fb[kHeld][2];
-  float s[FM] = {}, sa[FM];
-  const auto read_a = [&](int i) {
+  i32x4 fa[kSets][FM][2], fb[kSets][kHeld][2];
+  float s[FM] = {}, sa[kSets][FM];
+  const auto read_a = [&](int set, int i) {
 #pragma unroll
-    for (int h = 0; h < 2; h++) fa[i][h] = lds[(xa ^ (4 * h)) + i * 128];
+    for (int h = 0; h < 2; h++) fa[set][i][h] = lds[(xa ^ (4 * h)) + i * 128];
   };
-  const auto read_b = [&](int j) {
+  const auto read_b = [&](int set, int j) {
 #pragma unroll
-    for (int h = 0; h < 2; h++) fb[j % kHeld][h] = lds[(xb ^ (4 * h)) + (j / 2 * 32 + j % 2 * 4) * 8];
+    for (int h = 0; h < 2; h++)
+      fb[set][j % kHeld][h] = lds[(xb ^ (4 * h)) + (j / 2 * 32 + j % 2 * 4) * 8];
   };
   // the tokens' scales of a block
-  const auto read_scales = [&](uint32_t step) {
+  const auto read_scales = [&](int set, uint32_t step) {
     const float* const from = lsa[step / kChunk & 1] + (wm + p) * kChunk +
                               ((step % kChunk / 4 ^ p) & 1) * 4 + step % 4;
 #pragma unroll
-    for (int i = 0; i < FM; i++) sa[i] = from[i * 16 * kChunk];
+    for (int i = 0; i < FM; i++) sa[set][i] = from[i * 16 * kChunk];
   };
   // The weights' scales of this wave's channels, 64 blocks at a time: a word a
   // lane, in a place of the wave's own.
@@ -287,7 +289,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile_f8(F8Args g, Grid gr) 
   load_sb(64);
   offsets(0);
 #pragma unroll
-  for (uint32_t s = 0; s < (Turns ? S : S - 1); s++) {
+  for (uint32_t s = 0; s < S; s++) {
     if (s + 1 == steps && cut_last) offsets(s * kF8Step);
     end_buffer(ra, s, steps);
     end_buffer(rb, s, steps);
@@ -296,21 +298,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile_f8(F8Args g, Grid gr) 
       if (!Turns || s == 0 || i < LA || (i - LA) % 2 == 0)
         load(i, ra, rb, s < steps ? s * kF8Step : 0u, s * kStage * 16);
   }
-  arrived(std::integral_constant<int, Turns ? kEarly : kYoung>{});
+  arrived(std::integral_constant<int, Turns ? kEarly : kYoung + L>{});
   if (steps == 1 && cut_last) cut_stage(0);
   together();
 
   constexpr int kProducts = FM * FN, kLag = 2;
-  f32x4 d[4] = {};
-  // the x-th product of a stage, and the one before the last added to its sum
-  const auto multiply = [&](int x) {
-    d[x % 4] = block_sum(fb[x / FM % kHeld], fa[x % FM]);
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  const auto add = [&](int x) {
-    add_scaled(acc[x % FM][x / FM], d[x % 4], s[x % FM]);
-    here(acc[x % FM][x / FM]);
-  };
   uint32_t to = 0;                           // this stage's place, in pieces
   if constexpr (Turns) {
     // The two waves of a SIMD take turns: while one multiplies half a stage, the
@@ -323,6 +315,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile_f8(F8Args g, Grid gr) 
     // is loaded in turns 2 and 3, over the second half of b in turns 4 and 5; it has
     // arrived at the end of turn 7.
     const bool late = wave >= WM * WN / 2;
+    f32x4 d[4] = {};
+    // the x-th product of a stage, and the one before the last added to its sum
+    const auto multiply = [&](int x) {
+      d[x % 4] = block_sum(fb[0][x / FM % kHeld], fa[0][x % FM]);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    const auto add = [&](int x) {
+      add_scaled(acc[x % FM][x / FM], d[x % 4], s[x % FM]);
+      here(acc[x % FM][x / FM]);
+    };
     // loads n0 to n1 of `stage`
     const auto load_part = [&](int n0, int n1, uint32_t stage) {
       if (n0 == 0 && stage + 1 == steps && cut_last) offsets(stage * kF8Step);
@@ -355,21 +357,21 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile_f8(F8Args g, Grid gr) 
     for (uint32_t step = 0; step < steps; step++) {
       const float sb = read_sb(step);
 #pragma unroll
-      for (int j = 0; j < FN / 2; j++) read_b(j);
+      for (int j = 0; j < FN / 2; j++) read_b(0, j);
 #pragma unroll
-      for (int i = 0; i < FM; i++) read_a(i);
-      read_scales(step);
+      for (int i = 0; i < FM; i++) read_a(0, i);
+      read_scales(0, step);
       __builtin_amdgcn_sched_barrier(0);
       load_part(kEarly, L, step + 1);
 #pragma unroll
       for (int x = kProducts - kLag; x < kProducts; x++) add(x);
       together();
 #pragma unroll
-      for (int i = 0; i < FM; i++) s[i] = sa[i] * sb;
+      for (int i = 0; i < FM; i++) s[i] = sa[0][i] * sb;
       turn(0);
       together();
 #pragma unroll
-      for (int j = FN / 2; j < FN; j++) read_b(j);
+      for (int j = FN / 2; j < FN; j++) read_b(0, j);
       __builtin_amdgcn_sched_barrier(0);
       load_part(0, kEarly, step + 2);
 #pragma unroll
@@ -389,65 +391,69 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile_f8(F8Args g, Grid gr) 
     for (int x = kProducts - kLag; x < kProducts; x++) add(x);
     if (!late) together();
   } else {
-    // FN columns of FM products a stage, the results of one joined to the sums
-    // while the next ones run, the next column's codes read meanwhile.  Before the
-    // last column the next stage has arrived and everyone has read this one: then
-    // the next one's first codes are read, each over the one just used.  Over the
-    // place of the stage before this one the stage S - 1 after this one is loaded.
-    constexpr int kLoads = (L + FM * (FN - 1) - 1) / (FM * (FN - 1));   // a product
-    float sb = read_sb(0);
-    uint32_t free = (S - 1) * kStage;        // the place to load, in pieces
-    read_b(0);
+    // A stage's codes are read into registers while the one before it is
+    // multiplied.  At its start the next stage has arrived and everyone has read this
+    // one, over which the stage S after it is loaded.  The last results of a stage
+    // join the sums during the next one, with that one's scales.
+    f32x4 d[4] = {};
+    float old[FM];
+    constexpr int kReads = (2 * (FM + FN) + kProducts - 1) / kProducts;
+    constexpr int kLoads = (L + kProducts - 1) / kProducts;
+    float sb[2];
 #pragma unroll
-    for (int i = 0; i < FM; i++) read_a(i);
-    read_scales(0);
-    for (uint32_t step = 0; step < steps; step++) {
+    for (int j = 0; j < FN; j++) read_b(0, j);
 #pragma unroll
-      for (int i = 0; i < FM; i++) s[i] = sa[i] * sb;
-      const uint32_t next = to == (S - 1) * kStage ? 0 : to + kStage, coming = step + S - 1;
+    for (int i = 0; i < FM; i++) read_a(0, i);
+    read_scales(0, 0);
+    sb[0] = read_sb(0);
+    const auto stage = [&](uint32_t step, auto now) {
+      constexpr int P = decltype(now)::value;
+      const uint32_t next = to == (S - 1) * kStage ? 0 : to + kStage;
+      arrived(std::integral_constant<int, kYoung>{});
+      if (step + 2 == steps && cut_last) cut_stage(next);
+      together();
+      xa += next - to;
+      xb += next - to;
+      const uint32_t after = step + 1 < steps ? step + 1 : step, coming = step + S;
+#pragma unroll
+      for (int i = 0; i < FM; i++) {
+        old[i] = s[i];
+        s[i] = sa[P][i] * sb[P];
+      }
+      read_scales(1 - P, after);
+      sb[1 - P] = read_sb(after);
       if (coming + 1 == steps && cut_last) offsets(coming * kF8Step);
       end_buffer(ra, coming, steps);
       end_buffer(rb, coming, steps);
       const uint32_t k = coming < steps ? coming * kF8Step : 0u;
 #pragma unroll
-      for (int j = 0; j < FN; j++) {
-        if (j + 1 < FN) read_b(j + 1);
-        if (j + 2 == FN) {
-          const uint32_t after = step + 1 < steps ? step + 1 : step;
-          read_scales(after);
-          sb = read_sb(after);
-        }
-        if (j + 1 == FN) {
-          arrived(std::integral_constant<int, kYoung>{});
-          if (step + 2 == steps && cut_last) cut_stage(next);
-          together();
-          xa += next - to;
-          xb += next - to;
-        }
+      for (int x = 0; x < kProducts; x++) {
+        __builtin_amdgcn_sched_barrier(0);
+        d[x % 4] = block_sum(fb[P][x / FM], fa[P][x % FM]);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < FM; i++) {
-          const int x = j * FM + i;
-          __builtin_amdgcn_sched_barrier(0);
-          multiply(x);
-          if (j + 1 == FN) {
-            if (i == 0) read_b(0);
-            read_a(i);
-          } else {
+        for (int i = x * kReads; i < (x + 1) * kReads; i++)
+          if (i < FN) read_b(1 - P, i);
+          else if (i < FM + FN) read_a(1 - P, i - FN);
 #pragma unroll
-            for (int r = x * kLoads; r < (x + 1) * kLoads; r++)
-              if (r < L) load(r, ra, rb, k, free * 16);
-          }
-          if (x >= kLag) add(x - kLag);
-          __builtin_amdgcn_sched_barrier(0);
-        }
+        for (int r = x * kLoads; r < (x + 1) * kLoads; r++)
+          if (r < L) load(r, ra, rb, k, to * 16);
+        const int y = x < kLag ? kProducts - kLag + x : x - kLag;
+        add_scaled(acc[y % FM][y / FM], d[y % 4], x < kLag ? old[y % FM] : s[y % FM]);
+        here(acc[y % FM][y / FM]);
+        __builtin_amdgcn_sched_barrier(0);
       }
       if ((step + 1) % kChunk == 0) load_scales(rs, step / kChunk + 2);
       if (step % 64 == 63) load_sb(step + 65);
-#pragma unroll
-      for (int x = kProducts - kLag; x < kProducts; x++) add(x);
-      free = to;
       to = next;
+    };
+#pragma unroll 1
+    for (uint32_t step = 0; step < steps; step += 2) {
+      stage(step, std::integral_constant<int, 0>{});
+      if (step + 1 < steps) stage(step + 1, std::integral_constant<int, 1>{});
     }
+#pragma unroll
+    for (int y = kProducts - kLag; y < kProducts; y++) add_scaled(acc[y % FM][y / FM], d[y % 4], s[y % FM]);
   }
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt(0x0f70);        // nothing may still be on its way to LDS
