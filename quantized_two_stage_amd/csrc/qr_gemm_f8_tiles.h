@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cmath>
+#include <initializer_list>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -15,10 +16,11 @@ namespace qr {
 // `full` a block for each workgroup.  The weights' bytes take their time beside
 // that (6000 a ns where they are read once, else 5300): of the shorter of the two
 // `once` or `again` percent are added.
-// Fitted to the times of all tiles at 320 sizes (1 to 8192 tokens, sums and
-// channels of 64 to 16384, one product or 4 to 128 experts, cold weights); the
-// tile estimated to end first against the fastest at each: 1.00 at the median,
-// within 1.13 at nine of ten, 1.31 at worst (20 experts, 20 rows, 1664 x 640).
+// Fitted to the times of all tiles at 380 sizes (1 to 8192 tokens, sums and
+// channels of 64 to 16384, one product or 4 to 128 experts, cold weights).  The
+// tile that choose_f8_tile takes against the fastest at each, and at 100 more of
+// small groups: 1.00 at the median; one product within 1.11 at nine of ten and 1.45 at
+// worst, groups within 1.12 and 1.35.
 struct F8Tile {
   uint32_t bm, bn;                    // tokens and channels
   uint32_t wm, wn;                    // waves; wn == 0: wm waves that share the sum
@@ -27,16 +29,16 @@ struct F8Tile {
   uint32_t at_once, start, stage, more, full, once, again;
 };
 constexpr F8Tile kF8Tiles[] = {
-    {8, 16, 4, 0, 3, 1, 3, 3150, 59, 680, 31, 54, 77},
-    {16, 16, 8, 0, 2, 16, 2, 3270, 56, 1460, 31, 64, 90},
-    {16, 32, 4, 0, 3, 16, 2, 3220, 103, 2010, 43, 64, 82},
-    {32, 32, 4, 0, 2, 16, 2, 3310, 160, 3050, 28, 51, 70},
-    {64, 64, 2, 2, 4, 8, 2, 4050, 406, 2080, 246, 38, 81},
-    {64, 128, 2, 4, 5, 8, 1, 4660, 446, 730, 686, 24, 42},
-    {128, 64, 4, 2, 5, 8, 1, 4370, 467, 4290, 492, 30, 83},
-    {128, 128, 2, 4, 4, 8, 1, 5180, 582, 4380, 822, 30, 116},
-    {128, 256, 2, 4, 3, 8, 1, 6090, 848, 2820, 1508, 40, 120},
-    {256, 256, 4, 2, 2, 4, 1, 8240, 1208, 12040, 1268, 28, 25},
+    {8, 16, 4, 0, 3, 1, 3, 2860, 64, 350, 47, 54, 61},
+    {16, 16, 8, 0, 2, 16, 2, 2880, 50, 1590, 35, 83, 87},
+    {16, 32, 4, 0, 3, 16, 2, 3230, 97, 890, 85, 66, 80},
+    {32, 32, 4, 0, 2, 16, 2, 3440, 131, 2010, 48, 61, 83},
+    {64, 64, 2, 2, 4, 8, 2, 3930, 307, 120, 243, 44, 120},
+    {64, 128, 2, 4, 5, 8, 1, 4450, 422, 20, 404, 25, 78},
+    {128, 64, 4, 2, 5, 8, 1, 4370, 425, 4870, 148, 11, 85},
+    {128, 128, 2, 4, 4, 8, 1, 5280, 552, 2920, 598, 16, 120},
+    {128, 256, 2, 4, 3, 8, 1, 6640, 868, 790, 1145, 11, 97},
+    {256, 256, 4, 2, 2, 4, 1, 8080, 1162, 1450, 1423, 36, 119},
 };
 constexpr int kF8TileCount = sizeof(kF8Tiles) / sizeof(kF8Tiles[0]);
 constexpr uint32_t kF8Step = 128;     // codes of a block
@@ -64,7 +66,11 @@ constexpr bool f8_weights_once(uint32_t bm, uint32_t M, uint32_t E) {
   return E == 0 ? M <= bm : 2 * (uint64_t)M <= (uint64_t)bm * (E < M ? E : M);
 }
 
-inline double f8_estimate(const F8Tile& t, uint32_t M, uint32_t N, uint32_t K, uint32_t E) {
+struct F8Time {
+  double work, weights;               // of the products, of the weights' bytes
+  double all;
+};
+inline F8Time f8_estimate(const F8Tile& t, uint32_t M, uint32_t N, uint32_t K, uint32_t E) {
   const uint32_t steps = (K + kF8Step - 1) / kF8Step;
   const double blocks = (double)f8_tile_rows_likely(t.bm, M, E) * ((N + t.bn - 1) / t.bn);
   const double few = std::ceil(blocks / (256 * t.at_once)) * (t.start + (double)steps * t.stage);
@@ -75,16 +81,26 @@ inline double f8_estimate(const F8Tile& t, uint32_t M, uint32_t N, uint32_t K, u
   const bool once = f8_weights_once(t.bm, M, E);
   const double weights = hit * N * K / (once ? 6000 : 5300);
   const double more = 0.01 * (once ? t.once : t.again);
-  return work > weights ? work + weights * more : weights + work * more;
+  return {work, weights, work > weights ? work + weights * more : weights + work * more};
 }
 
 // Index into kF8Tiles.
 inline int choose_f8_tile(uint32_t M, uint32_t N, uint32_t K, uint32_t E) {
   if (E == 0 && M <= kF8Tiles[0].bm) return 0;
+  // Few rows an expert, and mostly weights to read: the smallest tile that reads
+  // them once.  The estimate alone takes wider ones there: 64 rows over 32 experts of
+  // 2048 x 8192 take 67 us in tiles of 8 x 16, 95 in 64 x 128.
+  if (E != 0)
+    for (int i : {0, 2, 3})
+      if (f8_weights_once(kF8Tiles[i].bm, M, E)) {
+        const F8Time t = f8_estimate(kF8Tiles[i], M, N, K, E);
+        if (t.weights >= 0.7 * t.work) return i;
+        break;
+      }
   int best = -1;
   double least = 0;
   for (int i = E == 0 ? 1 : 0; i < kF8TileCount; i++) {   // tiles of 8 rows: one row of them, or experts
-    const double ns = f8_estimate(kF8Tiles[i], M, N, K, E);
+    const double ns = f8_estimate(kF8Tiles[i], M, N, K, E).all;
     if (best < 0 || ns < least) {
       least = ns;
       best = i;

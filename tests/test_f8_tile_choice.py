@@ -17,9 +17,10 @@ def test_every_tile_is_reached():
 def test_edges_of_each_tile(tile):
     assert len(f8_tiles.tiles()) == 10
     found = [K for K in EDGES if tile in f8_tiles.smallest(K, 0) or tile in f8_tiles.smallest(K, 8)]
-    stages = f8_tiles.tiles()[tile][2]
-    assert any(K <= 128 * stages for K in found)              # a ring that is not filled
     assert any(K > 1024 for K in found)                       # scales in several parts
+    rows, channels, stages, _ = f8_tiles.tiles()[tile]
+    if (rows, channels) != (64, 128):                         # taken for sums of 2048 and more only
+        assert any(K <= 128 * stages for K in found)          # a ring that is not filled
 
 
 def test_small_batches_are_read_past_the_caches_only_once():
