@@ -98,7 +98,8 @@ int qr_gemm_f8(qr_dtype dtype, const uint8_t* a, size_t lda, const float* sa, si
  *   rows      M int32 in device memory: the row of a that row i takes.  A row
  *             may be taken any number of times; an index outside 0..tokens-1 (-1
  *             for padding) gives a row of c of zeros, without the bias
- *   b         E matrices N x K, row stride ldb, gb bytes apart (a multiple of 16)
+ *   b         E matrices N x K, row stride ldb, gb bytes apart (a multiple of 16;
+ *             one matrix ends before the next begins)
  *   sb        E matrices of block scales, row stride ldsb, gsb elements apart
  *   bias      E rows of N values, ldbias apart, or NULL
  *   offsets   E + 1 int32 in device memory, not falling, in 0..M.  Experts may be
@@ -107,8 +108,9 @@ int qr_gemm_f8(qr_dtype dtype, const uint8_t* a, size_t lda, const float* sa, si
  *             ones as equal; what such offsets make c is not defined, but
  *             nothing outside the arrays is touched
  *   c         M x N, row stride ldc
- * E in 1..QR_MAX_EXPERTS.  With rows, tokens * lda and 4 * tokens * ldsa must be
- * below 2^32 - 2^18 (rows are then addressed from a's start). */
+ * E in 1..QR_MAX_EXPERTS; (M / 256 + min(E, M)) * (N / 256) below 2^23, tiles of a
+ * launch.  With rows, tokens * lda and 4 * tokens * ldsa must be below 2^32 - 2^18
+ * (rows are then addressed from a's start). */
 int qr_gemm_f8_grouped(qr_dtype dtype, const uint8_t* a, size_t lda, const float* sa, size_t ldsa,
                        const int32_t* rows, size_t tokens, const uint8_t* b, size_t ldb, size_t gb,
                        const float* sb, size_t ldsb, size_t gsb, const void* bias, size_t ldbias,

@@ -8,6 +8,7 @@
 #include "qr_checks.h"
 #include "qr_f8.h"
 #include "qr_f8_internal.h"
+#include "qr_gemm_f8_tiles.h"
 
 namespace {
 
@@ -50,6 +51,14 @@ int check_product_sizes(size_t M, size_t N, size_t K) {
   if (N == 0 || N > kMaxRows) return fail(QR_ERR_SIZE, "N = %zu outside 1..%zu", N, kMaxRows);
   if (M > kMaxRows) return fail(QR_ERR_SIZE, "M = %zu exceeds %zu", M, kMaxRows);
   return QR_OK;
+}
+
+int launch_product(int dtype, const qr::F8Args& g, void* stream) {
+  const int tile = qr::choose_f8_tile(g.M, g.N, g.K, g.E);
+  if (tile < 0)
+    return fail(QR_ERR_SIZE, "M = %u, N = %u, E = %u: more tiles than a launch holds", g.M, g.N, g.E);
+  (void)hipGetLastError();
+  return hip_status(qr::launch_gemm_f8(tile, dtype, g, as_stream(stream)), "product launch");
 }
 
 int check_chosen(size_t T, size_t k) {
@@ -133,8 +142,7 @@ int qr_gemm_f8(qr_dtype dtype, const uint8_t* a, size_t lda, const float* sa, si
   const qr::F8Args g{a, lda, sa, ldsa, b, ldb, sb, ldsb, static_cast<const uint8_t*>(bias),
                      static_cast<uint8_t*>(c), ldc, (uint32_t)M, (uint32_t)N, (uint32_t)K,
                      0, (uint32_t)M, nullptr, nullptr, 0, 0, 0};
-  (void)hipGetLastError();
-  return hip_status(qr::launch_gemm_f8(dtype, g, as_stream(stream)), "product launch");
+  return launch_product(dtype, g, stream);
 }
 
 int qr_gemm_f8_grouped(qr_dtype dtype, const uint8_t* a, size_t lda, const float* sa, size_t ldsa,
@@ -177,8 +185,7 @@ int qr_gemm_f8_grouped(qr_dtype dtype, const uint8_t* a, size_t lda, const float
   const qr::F8Args g{a, lda, sa, ldsa, b, ldb, sb, ldsb, static_cast<const uint8_t*>(bias),
                      static_cast<uint8_t*>(c), ldc, (uint32_t)M, (uint32_t)N, (uint32_t)K,
                      (uint32_t)E, (uint32_t)tokens, offsets, rows, gb, gsb, ldbias};
-  (void)hipGetLastError();
-  return hip_status(qr::launch_gemm_f8(dtype, g, as_stream(stream)), "product launch");
+  return launch_product(dtype, g, stream);
 }
 
 size_t qr_route_workspace_bytes(size_t T, size_t E, size_t k) {

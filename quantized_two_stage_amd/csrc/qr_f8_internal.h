@@ -44,7 +44,8 @@ struct F8Args {
   size_t gb, gsb, ldbias;  // from one expert's weights, scales and bias to the next
 };
 
-hipError_t launch_gemm_f8(int dtype, const F8Args& g, hipStream_t st);
+// tile: choose_f8_tile of the sizes
+hipError_t launch_gemm_f8(int tile, int dtype, const F8Args& g, hipStream_t st);
 
 struct RouteArgs {
   const uint8_t* logits;

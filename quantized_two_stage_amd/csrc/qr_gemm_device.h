@@ -20,8 +20,8 @@ typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 // wrote its scalar operands: the compiler, which does not see the load, may restore
 // spilled ones (v_readlane_b32) right before the statement.
 // The buffer must be in scalar registers when it gets here: one that the compiler
-// holds in vector registers, because it cannot tell that all lanes hold the same
-// (see uniform), would be misread.
+// holds in vector registers, because it cannot tell that all lanes hold the same,
+// would be misread (a test reads the assembly for it).
 // Once: past the caches, for what no other workgroup reads.
 template <bool Once>
 __device__ __forceinline__ void load_to_lds(i32x4 rsrc, uint32_t lds, uint32_t voff,
@@ -43,12 +43,6 @@ __device__ __forceinline__ i32x4 buffer_at(const void* p) {
   const int lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
   const int hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)) & 0xffff;
   return i32x4{lo, hi, -1, 0x00027000};
-}
-// the same buffer, of which the compiler knows that all lanes hold the same
-__device__ __forceinline__ i32x4 uniform(i32x4 r) {
-#pragma unroll
-  for (int i = 0; i < 4; i++) r[i] = __builtin_amdgcn_readfirstlane(r[i]);
-  return r;
 }
 // all of the buffer while s < steps, afterwards nothing (and nothing is fetched)
 __device__ __forceinline__ void end_buffer(i32x4& r, uint32_t s, uint32_t steps) {

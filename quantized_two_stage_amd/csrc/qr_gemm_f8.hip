@@ -104,6 +104,8 @@ __device__ __forceinline__ bool find_job(const F8Args& g, Grid gr, Job& job) {
       uint32_t l, h;
       total += at(tiles_up_to(e, l, h), 63);
     }
+    // offsets that fall back again and again could ask for more than there are
+    total = total < gr.tm ? total : gr.tm;
     gr.tm = total;
     if (blockIdx.x >= total * gr.tn) return false;
     tile_of(gr, blockIdx.x, tm, tn);
@@ -660,9 +662,8 @@ Launch launch_of(int tile, std::integer_sequence<int, I...>) {
 
 }  // namespace
 
-hipError_t launch_gemm_f8(int dtype, const F8Args& g, hipStream_t st) {
-  return launch_of(choose_f8_tile(g.M, g.N, g.K, g.E),
-                   std::make_integer_sequence<int, kF8TileCount>{})(dtype, g, st);
+hipError_t launch_gemm_f8(int tile, int dtype, const F8Args& g, hipStream_t st) {
+  return launch_of(tile, std::make_integer_sequence<int, kF8TileCount>{})(dtype, g, st);
 }
 
 }  // namespace qr

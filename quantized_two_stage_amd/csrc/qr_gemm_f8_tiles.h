@@ -84,7 +84,13 @@ inline F8Time f8_estimate(const F8Tile& t, uint32_t M, uint32_t N, uint32_t K, u
   return {work, weights, work > weights ? work + weights * more : weights + work * more};
 }
 
-// Index into kF8Tiles.
+// A launch counts its lanes in 32 bits.
+constexpr bool f8_grid_fits(const F8Tile& t, uint32_t M, uint32_t N, uint32_t E) {
+  const uint64_t tiles = (uint64_t)f8_tile_rows(t.bm, M, E) * ((N + t.bn - 1) / t.bn);
+  return tiles * (64 * t.wm * (t.wn ? t.wn : 1)) < (uint64_t)1 << 32;
+}
+
+// Index into kF8Tiles; -1 if no tile's grid fits.
 inline int choose_f8_tile(uint32_t M, uint32_t N, uint32_t K, uint32_t E) {
   if (E == 0 && M <= kF8Tiles[0].bm) return 0;
   // Few rows an expert, and mostly weights to read: the smallest tile that reads
@@ -94,12 +100,13 @@ inline int choose_f8_tile(uint32_t M, uint32_t N, uint32_t K, uint32_t E) {
     for (int i : {0, 2, 3})
       if (f8_weights_once(kF8Tiles[i].bm, M, E)) {
         const F8Time t = f8_estimate(kF8Tiles[i], M, N, K, E);
-        if (t.weights >= 0.7 * t.work) return i;
+        if (t.weights >= 0.7 * t.work && f8_grid_fits(kF8Tiles[i], M, N, E)) return i;
         break;
       }
   int best = -1;
   double least = 0;
   for (int i = E == 0 ? 1 : 0; i < kF8TileCount; i++) {   // tiles of 8 rows: one row of them, or experts
+    if (!f8_grid_fits(kF8Tiles[i], M, N, E)) continue;
     const double ns = f8_estimate(kF8Tiles[i], M, N, K, E).all;
     if (best < 0 || ns < least) {
       least = ns;

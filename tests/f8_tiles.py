@@ -15,10 +15,17 @@ def program():
 
 
 @functools.lru_cache(None)
+def with_threads():
+    """(rows, channels, stages of a ring, threads of a workgroup)"""
+    out = subprocess.run([program(), "list"], capture_output=True, text=True, check=True).stdout
+    return [tuple(map(int, line.split()))[:3] + (int(line.split()[4]),) for line in out.splitlines()]
+
+
+@functools.lru_cache(None)
 def tiles():
     """(rows, channels, stages of a ring, waves along the channels or 0)"""
     out = subprocess.run([program(), "list"], capture_output=True, text=True, check=True).stdout
-    return [tuple(map(int, line.split())) for line in out.splitlines()]
+    return [tuple(map(int, line.split()))[:4] for line in out.splitlines()]
 
 
 def choices(sizes):

@@ -6,7 +6,7 @@
 
 int main(int argc, char**) {
   if (argc > 1) {
-    for (const qr::F8Tile& t : qr::kF8Tiles) std::printf("%u %u %u %u\n", t.bm, t.bn, t.stages, t.wn);
+    for (const qr::F8Tile& t : qr::kF8Tiles) std::printf("%u %u %u %u %u\n", t.bm, t.bn, t.stages, t.wn, 64 * t.wm * (t.wn ? t.wn : 1));
     return 0;
   }
   unsigned E, M, N, K;

@@ -117,6 +117,9 @@ def test_gemm_rejects(kw, code):
     (dict(bias=at(7)), ARG), (dict(c=at(6)), ARG), (dict(c=at(5)), ARG), (dict(c=at(2) + 304 * 200 * 4), ARG),
     (dict(tokens=1 << 20, lda=4096, b=1 << 50, sb=1 << 51, c=1 << 52, sa=1 << 49), SIZE),
     (dict(tokens=1 << 22, lda=304, ldsa=256, b=1 << 50, sb=1 << 51, c=1 << 52, sa=1 << 49), SIZE),
+    # more tiles than a launch holds
+    (dict(E=1024, M=1024, rows=None, K=16, lda=16, N=1 << 22, ldb=16, gb=1 << 26, gsb=3 << 15, ldc=1 << 22, sa=1 << 49,
+          b=1 << 50, sb=1 << 51, c=1 << 52), SIZE),
 ])
 def test_grouped_rejects(kw, code):
     assert _grouped(**kw) == code

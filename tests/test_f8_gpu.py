@@ -465,6 +465,22 @@ def test_grouped_bad_offsets_touch_nothing_outside(qr):
         assert only_rows_written(cbuf, M, N, N + 2, 9.0)
 
 
+@pytest.mark.parametrize("K", [64, 2048])
+def test_grouped_offsets_that_fall_again_and_again(qr, K):
+    """512 experts that all claim every row: more tiles than the grid has"""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    E, M, N = 1024, 600, 40
+    b = codes(N, K, g).view(torch.uint8).repeat(E, 1, 1).view(F8)
+    sb = scales_like(1, K, g).repeat(E, 1, 1)
+    a, sa = codes(M, K, g), scales_like(M, K, g)
+    offsets = torch.tensor([0, M] * 512 + [0], dtype=torch.int32, device="cuda")
+    cbuf, c = rows_in(M, N, N + 2, torch.float16, 9.0)
+    say("falling", K)
+    qr.qr_gemm_f8_grouped(a, sa, b, sb, offsets, c)
+    torch.cuda.synchronize()
+    assert only_rows_written(cbuf, M, N, N + 2, 9.0)
+
+
 # ---------------------------------------------------------------------------
 # router and combination
 

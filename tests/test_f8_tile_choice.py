@@ -28,3 +28,19 @@ def test_small_batches_are_read_past_the_caches_only_once():
     sizes = [(0, M, N, K) for M in (1, 8) for N in (16, 300, 8192) for K in (64, 16384)]
     assert set(f8_tiles.choices(sizes)) == {0}
     assert 0 not in f8_tiles.choices([(0, 9, N, K) for N in (16, 300, 8192) for K in (64, 16384)])
+
+
+def test_every_grid_fits_a_launch():
+    """lanes are counted in 32 bits: tiles that would need more are not taken, and no tile where all would"""
+    sizes = [(E, M, N, K) for E in (0, 1, 64, 1024) for M in (8, 512, 1024, 1 << 22) for K in (16, 8192)
+             for N in (1 << 16, 1 << 18, 1 << 20, 1 << 22)]
+    fits = {tile: 0 for tile in range(-1, 10)}
+    for (E, M, N, _), tile in zip(sizes, f8_tiles.choices(sizes)):
+        fits[tile] += 1
+        some = min(E, M)
+        for i, (rows, channels, _, threads) in enumerate(f8_tiles.with_threads()):
+            tiles = -(-M // rows) if E == 0 else (M - some) // rows + some
+            lanes = tiles * -(-N // channels) * threads
+            if i == tile or (tile == -1 and i == 9):
+                assert (lanes < 1 << 32) == (tile >= 0), (E, M, N, tile, lanes)
+    assert fits[-1] > 0 and fits[9] > 0
