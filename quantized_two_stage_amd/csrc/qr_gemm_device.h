@@ -86,15 +86,23 @@ struct Grid {
   uint32_t tm, tn, group;             // tiles along M and N; tile rows of a group
 };
 
-__device__ __forceinline__ void tile_of(const Grid& gr, uint32_t b, uint32_t& m, uint32_t& n) {
-  const uint32_t total = gr.tm * gr.tn, per = total / 8, extra = total % 8;
+// Workgroups go to the 8 XCDs in turn: the tile of workgroup b of `total`, so that
+// each XCD has neighbouring tiles.
+__device__ __forceinline__ uint32_t tile_number(uint32_t total, uint32_t b) {
+  const uint32_t per = total / 8, extra = total % 8;
   const uint32_t x = b % 8, i = b / 8;
-  const uint32_t t = x * per + (x < extra ? x : extra) + i;
+  return x * per + (x < extra ? x : extra) + i;
+}
+// the t-th tile, down the rows of a group of tile rows first
+__device__ __forceinline__ void tile_at(const Grid& gr, uint32_t t, uint32_t& m, uint32_t& n) {
   const uint32_t g = t / (gr.group * gr.tn), r = t % (gr.group * gr.tn);
   const uint32_t m0 = g * gr.group;
   const uint32_t rows = gr.tm - m0 < gr.group ? gr.tm - m0 : gr.group;
   m = m0 + r % rows;
   n = r / rows;
+}
+__device__ __forceinline__ void tile_of(const Grid& gr, uint32_t b, uint32_t& m, uint32_t& n) {
+  tile_at(gr, tile_number(gr.tm * gr.tn, b), m, n);
 }
 
 }  // namespace
