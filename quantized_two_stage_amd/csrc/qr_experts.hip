@@ -18,6 +18,16 @@ namespace {
 // launch chooses and counts (k_choose, a workgroup for `turns` times 64 tokens),
 // and a second one adds up the counts before its tokens' and places the rows
 // (k_place); there are at most kMaxChunks counts of an expert to add.
+//
+// A token's k experts are k times the largest of its logits, held as ordered keys
+// in the registers of a few lanes; weights are exponentials of differences to the
+// largest logit, so nothing overflows, summed in binary32.
+//
+// Bound by the chain of k reductions over a group's lanes, short calls by the launch.
+// Measured: 16 tokens over 32 experts, k = 4: 4.0 us; 16384 over 256, k = 8, bf16:
+// 18.7 us (k_choose 11, k_place 7.5), 4096 over 512: 18; the bytes alone would take 2.
+// Placing the rows in a second launch costs about 2.5 us, but its workgroups need
+// all the counts, and no workgroup may wait for another.
 
 constexpr uint32_t kTokens = 64;           // of a turn
 constexpr uint32_t kMaxChunks = 256;
@@ -362,8 +372,11 @@ hipError_t route_by_experts(const RouteArgs& a, hipStream_t st) {
 constexpr uint32_t kSumWaves = 4;          // of a workgroup
 constexpr uint32_t kAtOnce = 8;            // rows on their way at a time
 
-// A wave takes 64 vectors of 8 values of one token's row: `pieces` waves to a
-// token.
+// y = sum_j weights[j] * c[place[j]] + addend in binary32, rounded once.  A wave
+// takes 64 vectors of 8 values of one token's row (`pieces` waves to a token), and
+// has up to 8 rows' vectors on their way.  Bound by HBM: 4096 tokens, k = 8, 8192
+// bf16 122 us, 4.95 TB/s (a copy 5.2); k = 2 51 us, 5.3 TB/s; 17 x 5003 4.0 us, a
+// launch with two dependent reads.
 template <int D, int E>
 __global__ __launch_bounds__(64 * kSumWaves) void k_combine(CombineArgs a, uint32_t pieces,
                                                            uint32_t waves) {

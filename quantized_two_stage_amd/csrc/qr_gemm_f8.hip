@@ -2,16 +2,34 @@
 // (include/qr_f8.h): matrix products of E4M3FN codes with a scale for each block
 // of 128, the tokens in one group or grouped by expert.
 //
-// A block's sum is one matrix instruction (16x16x128): it starts from zero, and
-// its four results a lane are multiplied by the token's scale times the weights'
-// block scale and added to binary32 sums with one fused multiply-add each, while
-// the matrix unit works on the next.  Stages of the sum are therefore blocks.
-// Loads, rings, swizzle and the two kernels (k_split, k_tile) are as in
-// qr_gemm.hip; the tokens' scales pass through LDS beside the codes, the
-// weights' through the scalar cache.
+// c = sum_kb (sum_{k in kb} a[m][k] * b[n][k]) * (sa[m][kb] * sb[n/128][kb]) + bias.
+// A block's sum is one matrix instruction (16x16x128, 32 cycles): it starts from
+// zero, and its four results a lane are multiplied by the token's scale times the
+// weights' block scale and added to binary32 sums with one fused multiply-add each,
+// while the matrix unit works on the next (33.7 cycles a product with them, from
+// registers).  Stages of the sum are therefore blocks.  Loads, rings, swizzle and
+// the two kernels (k_split, k_tile) are as in qr_gemm.hip; the tokens' and the
+// weights' scales pass through LDS beside the codes (of k_split the weights'
+// through the scalar cache).
+//
+// The one rounding to fewer than 32 bits is c's; the matrix unit's own cut of the
+// products is in include/qr_f8.h.
 //
 // By experts: the grid has a workgroup for every tile that there may be; each
-// finds its expert and rows from the offsets.
+// finds its expert and rows from the offsets.  Nothing is read back by the host.
+//
+// Measured (cold weights; a copy reaches 5.2 TB/s, plain reads 6.8, a library
+// product of 8192^3 such codes with one scale for all 382 us):
+//   1 token, 8192 x 8192       12 to 14 us, 4.8 to 5.6 TB/s: the weights' bytes
+//   8192^3, bias               435 to 480 us on several cards, 2.29 to 2.53 PFLOP/s;
+//                              on one of them the library's took 418 us, this 479.
+//                              The matrix units are busy 65% of the time
+//   16 tokens over 4 of 32 experts of 2048 x 8192   69 us, 6.6 TB/s of the 454 MB
+//                              of the 27 experts hit (63 with some in the cache)
+//   4096 tokens over 8 of 64 experts of 8192 x 1024   455 to 510 us, 1.1 to 1.2
+//                              PFLOP/s, 2.4 TB/s: sums of 8 blocks, between which a
+//                              CU loads its first stage and writes 128 KB of c with
+//                              its matrix units idle (35% busy)
 #include <type_traits>
 #include <utility>
 
@@ -156,7 +174,10 @@ __device__ __forceinline__ size_t first_row(const F8Args& g, const Job& job) {
 }
 
 // A BM x BN tile to a workgroup of WM x WN waves, through a ring of S stages of
-// one block each.
+// one block each.  Bound by the loads to LDS up to 128 x 128 (60 bytes/ns a CU), at
+// 256 x 256 by the matrix units, and by its ends where sums are short: a tile of 256
+// x 256 takes 1.67 us a block and 9 us besides (8192 x 8192: K = 512 63 us, K = 8192
+// 465 on the same card).
 //
 // The tokens' scales come 8 blocks at a time (two 16-byte pieces a row), one load
 // a lane, into the one of two buffers that is not in use.
@@ -490,8 +511,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_tile_f8(F8Args g, Grid gr) 
 }
 
 // A block of BM tokens by BN channels to a workgroup, whose W waves share the
-// sum: wave w takes blocks w, w + W, ... through a ring of S stages of its own in
-// LDS, the tokens' scales beside the codes.
+// sum (few tiles, or few rows an expert: bound by the weights' bytes, or by the
+// latency of a stage, 0.05 to 0.13 us): wave w takes blocks w, w + W, ... through a
+// ring of S stages of its own in LDS, the tokens' scales beside the codes.
 constexpr uint32_t kApart = 2;               // stages from one tile's start to its neighbour's
 
 template <int BM, int BN, int W, int S, int D, bool Once, bool Grouped>
