@@ -487,6 +487,16 @@ def _pieces(what, t, rows, cols, dtype, dev, piece):
     return ld
 
 
+def _table(what, t, rows, cols, dtype, dev):
+    """A contiguous matrix argument."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != (rows, cols):
+        _refuse(what, t, dtype, dev,
+                "%s has shape %s: %s expected" % (what, tuple(t.shape), (rows, cols)))
+    if not t.is_contiguous():
+        raise ValueError("%s is not contiguous" % what)
+    return t.data_ptr()
+
+
 def qr_add_rmsnorm_f8(x, residual, weight, eps, h, y, q, scales, stream=None):
     """h = x + residual; q, scales = the e4m3 codes and block scales of h's
     root-mean-square norm times weight; y (or None) these values in 16 bits.
@@ -592,14 +602,12 @@ def qr_route(logits, weights, experts, offsets, rows, place, renormalize=False, 
         raise TypeError("logits are %s: float16, bfloat16 or float32 expected" % logits.dtype)
     dev = _device(logits, "logits")
     k = _matrix_shape("weights", weights)[1]
-    for what, t, dtype in (("weights", weights, torch.float32), ("experts", experts, torch.int32),
-                           ("place", place, torch.int32)):
-        _mat(what, t, T, k, dtype, dev)
-        _vec(what, t, T * k, dtype, dev)
     _check(LIB.qr_route(
         code, logits.data_ptr(), _ld("logits", logits, T, E), T, E, k, int(bool(renormalize)),
-        weights.data_ptr(), experts.data_ptr(), _vec("offsets", offsets, E + 1, torch.int32, dev),
-        _vec("rows", rows, T * k, torch.int32, dev), place.data_ptr(),
+        _table("weights", weights, T, k, torch.float32, dev),
+        _table("experts", experts, T, k, torch.int32, dev),
+        _vec("offsets", offsets, E + 1, torch.int32, dev),
+        _vec("rows", rows, T * k, torch.int32, dev), _table("place", place, T, k, torch.int32, dev),
         workspace.data_ptr() if workspace is not None else None, _workspace_bytes(workspace, dev),
         _stream_on(dev, stream)))
     return weights, experts, offsets, rows, place
@@ -613,12 +621,11 @@ def qr_combine(c, place, weights, y, addend=None, stream=None):
     code = _type16(c, "c")
     dev = _device(y, "y")
     T, k = _matrix_shape("place", place)
-    _mat("weights", weights, T, k, torch.float32, dev)
     lda = _mat("addend", addend, T, d, c.dtype, dev) if addend is not None else 0
     _check(LIB.qr_combine(
         code, c.data_ptr(), _mat("c", c, R, d, c.dtype, dev), R,
         _vec("place", place, T * k, torch.int32, dev),
-        _vec("weights", weights, T * k, torch.float32, dev), T, k, d,
+        _table("weights", weights, T, k, torch.float32, dev), T, k, d,
         addend.data_ptr() if addend is not None else None, lda, y.data_ptr(),
         _mat("y", y, T, d, c.dtype, dev), _stream_on(dev, stream)))
     return y
