@@ -389,7 +389,7 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_combine(CombineArgs a, uint3
   const int32_t* const place = a.place + (size_t)t * a.k;
   const float* const weights = a.weights + (size_t)t * a.k;
   u32x4 add = {0u, 0u, 0u, 0u};
-  if (a.addend) add = load_vec<E>(a.addend + 2 * ((size_t)t * a.lda + i0), n);
+  if (a.addend) add = load_raw<E>(a.addend + 2 * ((size_t)t * a.lda + i0), n);
   float y[8] = {};
   for (uint32_t j0 = 0; j0 < a.k; j0 += kAtOnce) {
     u32x4 v[kAtOnce];
@@ -397,21 +397,21 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_combine(CombineArgs a, uint3
 #pragma unroll
     for (uint32_t j = 0; j < kAtOnce; j++) {
       row[j] = j0 + j < a.k ? (uint32_t)place[j0 + j] : ~0u;
-      if (row[j] < a.R) v[j] = load_vec<E>(a.c + 2 * ((size_t)row[j] * a.ldc + i0), n);
+      if (row[j] < a.R) v[j] = load_raw<E>(a.c + 2 * ((size_t)row[j] * a.ldc + i0), n);
     }
 #pragma unroll
     for (uint32_t j = 0; j < kAtOnce; j++)
       if (row[j] < a.R) {
         const float s = weights[j0 + j];
         float f[8];
-        widen<D>(v[j], f);
+        widen<D>(from_raw<E>(v[j], n), f);
 #pragma unroll
         for (int i = 0; i < 8; i++) y[i] = __builtin_fmaf(s, f[i], y[i]);
       }
   }
   if (a.addend) {
     float f[8];
-    widen<D>(add, f);
+    widen<D>(from_raw<E>(add, n), f);
 #pragma unroll
     for (int i = 0; i < 8; i++) y[i] += f[i];
   }

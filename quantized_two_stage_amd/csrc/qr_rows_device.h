@@ -24,10 +24,14 @@ __device__ __forceinline__ void store8(uint8_t* p, u32x4 v) { __builtin_memcpy(p
 
 // The first n values of the vector at p, zeros after them.  Rows of 8 values or
 // more: a row's last, short vector is read as the 16 bytes that end where the
-// row ends and shifted down, one load whatever n is.
-__device__ __forceinline__ u32x4 load_n(const uint8_t* p, uint32_t n) {
+// row ends (load_ending) and shifted down (shifted), one load whatever n is.  All
+// of a lane's loads come before the first shift: a shift between them waits for
+// the load before it (the norm of 3000 x 5003 took 37 us so, now 31.5).
+__device__ __forceinline__ u32x4 load_ending(const uint8_t* p, uint32_t n) {
+  return load8(p - 2 * (8 - n));
+}
+__device__ __forceinline__ u32x4 shifted(u32x4 v, uint32_t n) {
   const uint32_t miss = 8 - n;
-  u32x4 v = load8(p - 2 * miss);
   if (miss != 0) {
     uint64_t lo = v.x | (uint64_t)v.y << 32, hi = v.z | (uint64_t)v.w << 32;
     if (miss >= 4) {
@@ -40,6 +44,9 @@ __device__ __forceinline__ u32x4 load_n(const uint8_t* p, uint32_t n) {
     v = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
   }
   return v;
+}
+__device__ __forceinline__ u32x4 load_n(const uint8_t* p, uint32_t n) {
+  return shifted(load_ending(p, n), n);
 }
 // the same, value by value, for rows of any length
 __device__ __forceinline__ u32x4 load_each(const uint8_t* p, uint32_t n) {
@@ -60,17 +67,34 @@ template <int E>
 __device__ __forceinline__ u32x4 load_vec(const uint8_t* p, uint32_t n) {
   return E == kWhole ? load8(p) : E == kShort ? load_n(p, n) : load_each(p, n);
 }
+// the same in two steps
+template <int E>
+__device__ __forceinline__ u32x4 load_raw(const uint8_t* p, uint32_t n) {
+  return E == kWhole ? load8(p) : E == kShort ? load_ending(p, n) : load_each(p, n);
+}
+template <int E>
+__device__ __forceinline__ u32x4 from_raw(u32x4 v, uint32_t n) {
+  return E == kShort ? shifted(v, n) : v;
+}
 template <int E>
 __device__ __forceinline__ void store_vec(uint8_t* p, u32x4 v, uint32_t n) {
   if (E == kWhole || n == 8) {
     store8(p, v);
     return;
   }
-  const uint64_t lo = v.x | (uint64_t)v.y << 32, hi = v.z | (uint64_t)v.w << 32;
-#pragma unroll 1
-  for (uint32_t i = 0; i < n; i++)
-    reinterpret_cast<uint16_t*>(p)[i] =
-        (uint16_t)(i < 4 ? lo >> (16 * i) : hi >> (16 * (i - 4)));
+  uint64_t lo = v.x | (uint64_t)v.y << 32;
+  if (n & 4) {
+    __builtin_memcpy(p, &lo, 8);
+    p += 8;
+    lo = v.z | (uint64_t)v.w << 32;
+  }
+  if (n & 2) {
+    const uint32_t two = (uint32_t)lo;
+    __builtin_memcpy(p, &two, 4);
+    p += 4;
+    lo >>= 32;
+  }
+  if (n & 1) *reinterpret_cast<uint16_t*>(p) = (uint16_t)lo;
 }
 
 template <int D>
@@ -145,7 +169,7 @@ struct Norm {
   template <int E>
   __device__ __forceinline__ void load(const Row& r, uint32_t vec, uint32_t n, Raw& v) const {
     if constexpr (C < 0) {
-      v.x = load_vec<E>(r.x + 16 * (size_t)vec, n);
+      v.x = load_raw<E>(r.x + 16 * (size_t)vec, n);
     } else if constexpr (C == kFP) {
       v.x = load8(r.x + 16 * (size_t)(r.vec0 + vec));
     } else {
@@ -155,8 +179,8 @@ struct Norm {
       if constexpr (CodecT<C>::asym)
         v.z = reinterpret_cast<const uint16_t*>(r.x + a.off_z)[q >> 2];
     }
-    if (r.res) v.res = load_vec<E>(r.res + 16 * (size_t)vec, n);
-    v.w = load_vec<E>(a.weight + 16 * (size_t)vec, n);
+    if (r.res) v.res = load_raw<E>(r.res + 16 * (size_t)vec, n);
+    v.w = load_raw<E>(a.weight + 16 * (size_t)vec, n);
   }
   // u and the sum of squares, and h written
   template <int E>
@@ -164,7 +188,7 @@ struct Norm {
                                          float (&u)[8], float& ss) const {
     u32x4 h;
     if constexpr (C < 0) {
-      h = v.x;
+      h = from_raw<E>(v.x, n);
     } else if constexpr (C == kFP) {
       h = v.x;
       if constexpr (D == kBF16H)
@@ -187,14 +211,14 @@ struct Norm {
     widen<B>(h, hv);
     if (r.res) {
       float rv[8];
-      widen<B>(v.res, rv);
+      widen<B>(from_raw<E>(v.res, n), rv);
 #pragma unroll
       for (int k = 0; k < 4; k++)
         h[k] = st16x2<B>(hv[2 * k] + rv[2 * k], hv[2 * k + 1] + rv[2 * k + 1]);
       widen<B>(h, hv);
     }
     if (r.h) store_vec<E>(r.h + 16 * (size_t)vec, h, n);
-    weigh(hv, v.w, u, ss);
+    weigh(hv, from_raw<E>(v.w, n), u, ss);
   }
   __device__ __forceinline__ void weigh(const float (&hv)[8], u32x4 w, float (&u)[8],
                                         float& ss) const {
@@ -238,8 +262,8 @@ struct Silu {
   }
   template <int E>
   __device__ __forceinline__ void load(const Row& r, uint32_t vec, uint32_t n, Raw& v) const {
-    v.g = load_vec<E>(r.g + 16 * (size_t)vec, n);
-    v.u = load_vec<E>(r.u + 16 * (size_t)vec, n);
+    v.g = load_raw<E>(r.g + 16 * (size_t)vec, n);
+    v.u = load_raw<E>(r.u + 16 * (size_t)vec, n);
   }
   // exp(-x) for 0 <= x <= 500: v_exp_f32 (2^hi, within one unit) of the rounded
   // hi = -x*log2(e), times 1 + rest, rest = -x - hi*ln 2.  A rounded exponent
@@ -265,12 +289,12 @@ struct Silu {
   // (inf * 0 among them).  8192 rows of 4096, bf16: 31.4 us, and 32.5 where
   // every wave has a gate beyond.
   template <int E>
-  __device__ __forceinline__ void values(const Row&, uint32_t, uint32_t, const Raw& v,
+  __device__ __forceinline__ void values(const Row&, uint32_t, uint32_t n, const Raw& v,
                                          float (&u)[8], float&) const {
     constexpr float kFar = 64.0f;
     float g[8];
-    widen<D>(v.g, g);
-    widen<D>(v.u, u);
+    widen<D>(from_raw<E>(v.g, n), g);
+    widen<D>(from_raw<E>(v.u, n), u);
     float most = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; i++) most = max_abs(most, g[i]);
@@ -366,9 +390,19 @@ __device__ __forceinline__ void store_codes(int8_t* p, u32x2 w, uint32_t n) {
   if (E == kWhole || n == 8) {
     __builtin_memcpy(p, &w, 8);
   } else {
-    const uint64_t v = w.x | (uint64_t)w.y << 32;
-#pragma unroll 1
-    for (uint32_t i = 0; i < n; i++) p[i] = (int8_t)(v >> (8 * i));
+    uint32_t v = w.x;
+    if (n & 4) {
+      __builtin_memcpy(p, &v, 4);
+      p += 4;
+      v = w.y;
+    }
+    if (n & 2) {
+      const uint16_t two = (uint16_t)v;
+      __builtin_memcpy(p, &two, 2);
+      p += 2;
+      v >>= 16;
+    }
+    if (n & 1) *p = (int8_t)v;
   }
 }
 

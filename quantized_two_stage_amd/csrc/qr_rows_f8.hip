@@ -14,8 +14,8 @@
 // inputs; a copy reaches 5.2 TB/s):
 //   norm, 8192 x 8192 bf16 with h and y   112 us, 5.4 TB/s; without y 91, 5.2 TB/s
 //   norm, 1 x 8192                        3.9 us (an empty launch with one read 2.2)
-//   norm, 3000 x 5003 fp16                37 us, 2.8 TB/s: rows that start at any even
-//                                         byte take their loads and stores across lines
+//   norm, 3000 x 5003 fp16                31.5 us, 3.35 TB/s (3000 x 5000 27.5): rows that
+//                                         start at any even byte are read across lines
 //   activation, 8192 x 4096 bf16          34.7 us, 4.9 TB/s
 //   activation, 32768 x 1024 bf16         36.4 us, 4.6 TB/s; 333 x 1000 3.3 us
 #include "qr_f8.h"
