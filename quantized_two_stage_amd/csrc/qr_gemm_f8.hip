@@ -19,11 +19,11 @@
 // finds its expert and rows from the offsets.  Nothing is read back by the host.
 //
 // Measured (cold weights; a copy reaches 5.2 TB/s, plain reads 6.8, a library
-// product of 8192^3 such codes with one scale for all 382 us):
+// product of 8192^3 such codes with one scale for all 355 to 418 us):
 //   1 token, 8192 x 8192       12 to 14 us, 4.8 to 5.6 TB/s: the weights' bytes
 //   8192^3, bias               435 to 480 us on several cards, 2.29 to 2.53 PFLOP/s;
-//                              on one of them the library's took 418 us, this 479.
-//                              The matrix units are busy 65% of the time
+//                              (the library's 382 where this took 447); the
+//                              matrix units are busy 65% of the time
 //   16 tokens over 4 of 32 experts of 2048 x 8192   69 us, 6.6 TB/s of the 454 MB
 //                              of the 27 experts hit (63 with some in the cache)
 //   4096 tokens over 8 of 64 experts of 8192 x 1024   455 to 510 us, 1.1 to 1.2
