@@ -28,7 +28,7 @@ struct Rows {
   size_t bytes() const { return ((rows - 1) * ld + cols) * elem; }
 };
 
-// longest row stride: keeps every extent far below 2^64 bytes
+// longest row stride: keeps every extent below 2^64 bytes, though not its end
 constexpr size_t kMaxStride = (size_t)1 << 40;
 constexpr size_t kMaxRows = (size_t)1 << 22;
 
@@ -45,7 +45,7 @@ inline int check(const Rows& r) {
 // another (columns of one buffer).
 inline bool overlap(const Rows& a, const Rows& b) {
   const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-  if (x >= y + b.bytes() || y >= x + a.bytes()) return false;
+  if (x >= y ? x - y >= b.bytes() : y - x >= a.bytes()) return false;
   const size_t stride = a.ld * a.elem;
   if (stride != b.ld * b.elem) return true;
   const size_t at = y >= x ? (y - x) % stride : stride - 1 - (x - y - 1) % stride;
