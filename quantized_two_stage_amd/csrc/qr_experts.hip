@@ -340,14 +340,20 @@ Chunks chunks_of(uint32_t T) {
   return Chunks{turns, turns ? (all + turns - 1) / turns : 0u};
 }
 
+// G lanes to a token, V logits to a lane: at most G * V experts.
+template <int D, int G, int V>
+hipError_t route_at_once(const RouteArgs& a, hipStream_t st) {
+  if constexpr (G * V <= 256)              // a lane to an expert
+    if (a.T * G <= 256) {                  // a launch of few waves starts sooner
+      k_choose<D, G, V, 256, true><<<1, 256, 0, st>>>(a, 1);
+      return hipGetLastError();
+    }
+  k_choose<D, G, V, kLanes, true><<<1, kLanes, 0, st>>>(a, 1);
+  return hipGetLastError();
+}
 template <int D, int G, int V>
 hipError_t route(const RouteArgs& a, hipStream_t st) {
-  if (a.T <= kTokens) {
-    // a launch of few waves starts sooner
-    if (a.E <= 256 && a.T * G <= 256) k_choose<D, G, V, 256, true><<<1, 256, 0, st>>>(a, 1);
-    else k_choose<D, G, V, kLanes, true><<<1, kLanes, 0, st>>>(a, 1);
-    return hipGetLastError();
-  }
+  if (a.T <= kTokens) return route_at_once<D, G, V>(a, st);
   const Chunks c = chunks_of(a.T);
   k_choose<D, G, V, kLanes, false><<<c.count, kLanes, 0, st>>>(a, c.turns);
   const hipError_t e = hipGetLastError();
@@ -362,7 +368,7 @@ hipError_t route_by_experts(const RouteArgs& a, hipStream_t st) {
   if (a.E <= 64) return route<D, 8, 8>(a, st);
   if (a.E <= 128) return route<D, 16, 8>(a, st);
   if (a.E <= 256) return route<D, 16, 16>(a, st);
-  if (a.E <= 512) return a.T <= 16 ? route<D, 64, 8>(a, st) : route<D, 16, 32>(a, st);
+  if (a.E <= 512) return a.T <= 16 ? route_at_once<D, 64, 8>(a, st) : route<D, 16, 32>(a, st);
   return route<D, 64, 16>(a, st);
 }
 
