@@ -670,7 +670,9 @@ hipError_t launch_tile(int dtype, const F8Args& g, hipStream_t st) {
   const auto of_type = [&](auto d) {
     const bool once = f8_weights_once(t.bm, g.M, g.E);
     if (g.E == 0) {
-      if (once) kernel(d, std::true_type{}, std::false_type{});
+      // tiles of 8 rows: up to 8 tokens only (choose_f8_tile)
+      if constexpr (t.bm == 8) kernel(d, std::true_type{}, std::false_type{});
+      else if (once) kernel(d, std::true_type{}, std::false_type{});
       else kernel(d, std::false_type{}, std::false_type{});
     } else {
       if (once) kernel(d, std::true_type{}, std::true_type{});

@@ -1,6 +1,8 @@
 """Which kernels of include/qr_f8.h the library holds: those that a call can reach, and no others (no GPU needed)."""
 import re
 
+import f8_tiles
+
 from quantized_two_stage_amd import qr
 
 TYPES = (0, 1)                                       # of 16 bits
@@ -26,3 +28,14 @@ def test_router():
                 lanes = 256 if T <= 64 and E <= 256 and T * G <= 256 else 1024
                 reached.add((dtype, G, V, lanes, int(T <= 64)))
     assert held("k_choose", *"iiiib") == reached
+
+
+def test_products():
+    split, tile = held("k_split_f8", *"iiiiibb"), held("k_tile_f8", *"iiiiiibb")
+    assert {x[:2] for x in split | tile} == {t[:2] for t in f8_tiles.tiles()}
+    # one product takes tiles of 8 rows up to 8 tokens only, whose weights are read by one workgroup alone
+    assert {x[5:] for x in split if x[0] == 8} == {(1, 0), (1, 1), (0, 1)}
+    for kernels in (split, tile):
+        for x in kernels:
+            if x[0] != 8:
+                assert {x[:-2] + (once, grouped) for once in (0, 1) for grouped in (0, 1)} <= kernels
