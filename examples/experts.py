@@ -49,7 +49,8 @@ def codes_of(w):
     b = in_blocks(w)
     scale = b.abs().amax((-3, -1)) / 448
     codes = torch.empty(*w.shape[:-1], -(-K // 16) * 16, dtype=torch.float8_e4m3fn, device=w.device)[..., :K]
-    codes.copy_((b / scale[..., :, None, :, None]).flatten(-2).flatten(-3, -2)[..., :N, :K])
+    divisor = torch.where(scale > 0, scale, 1.0)             # a block of zeros has codes 0 and scale 0
+    codes.copy_((b / divisor[..., :, None, :, None]).flatten(-2).flatten(-3, -2)[..., :N, :K])
     return codes, scale
 
 
