@@ -1,0 +1,4 @@
+"""Sizes of tests/test_f8_edges_gpu.py, which tests/test_f8_edges.py asks the launch's own rule about."""
+# (E, M, N, K): more than 64 experts, 256 x 256 tiles
+MANY = [(70, 12000, 2100, 1152), (72, 14896, 2302, 1176), (70, 6000, 4096, 144), (130, 20000, 1100, 520),
+        (300, 30000, 1030, 272)]

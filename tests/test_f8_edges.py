@@ -1,0 +1,16 @@
+"""The sizes of the GPU tests of the products' tiles do run what they are meant to (no GPU needed)."""
+import f8_tiles
+from f8_edges import MANY
+from test_f8_tile_choice import EDGES
+
+
+def test_every_tile_has_a_size_in_the_tests():
+    """of test_f8_tiles_gpu.py, which passes over what has none"""
+    without = [(tile, E) for E in (0, 1, 8, 70) for tile in range(10)
+               if not any(tile in f8_tiles.smallest(K, E) for K in EDGES)]
+    assert without == [(9, 70)]                      # MANY instead
+
+
+def test_many_experts_in_large_tiles():
+    assert {f8_tiles.tiles()[t][:2] for t in f8_tiles.choices(MANY)} == {(256, 256)}
+    assert all(E > 64 for E, *_ in MANY) and any(E > 128 for E, *_ in MANY)

@@ -2,9 +2,38 @@
 import pytest
 import torch
 
-from test_f8_gpu import F8, qr, say  # noqa: F401
+from f8_edges import MANY
+from test_f8_gpu import (F8, blocks, check_product, codes, qr, reference, rows_in, say, scales_like,  # noqa: F401
+                         sizes_of_groups)
 
 pytestmark = pytest.mark.gpu
+
+
+def check_groups(c, a, sa, rows, b, sb, offsets, label):
+    ends = offsets.tolist()
+    for e in range(b.shape[0]):
+        lo, hi = ends[e], ends[e + 1]
+        if lo < hi:
+            at = rows[lo:hi].long()
+            check_product(c[lo:hi], *reference(a.view(torch.uint8)[at].view(F8), sa[at], b[e], sb[e], None), (*label, e))
+
+
+@pytest.mark.parametrize("kind", ["random", "short"])
+@pytest.mark.parametrize("E,M,N,K", MANY)
+def test_large_tiles_of_many_experts(qr, E, M, N, K, kind):  # noqa: F811
+    """more experts than a wave adds up at a time, in tiles of 256 x 256"""
+    say("many experts", E, M, N, K, kind)
+    g = torch.Generator(device="cuda").manual_seed(E + M + N + K)
+    tokens = M // 3
+    a, sa = codes(tokens, K, g), scales_like(tokens, K, g)
+    b, sb = codes(E * N, K, g).unflatten(0, (E, N)), scales_like(E * blocks(N), K, g).unflatten(0, (E, blocks(N)))
+    offsets = sizes_of_groups(kind, E, M, g)
+    rows = torch.randint(0, tokens, (M,), generator=g, device="cuda").to(torch.int32)
+    _, c = rows_in(M, N, N + 1, torch.bfloat16, 9.0)
+    qr.qr_gemm_f8_grouped(a, sa, b, sb, offsets, c, rows=rows)
+    lo, hi = int(offsets[0]), int(offsets[-1])
+    assert bool((c[:lo] == 9.0).all()) and bool((c[hi:] == 9.0).all())
+    check_groups(c, a, sa, rows, b, sb, offsets, (E, M, N, K))
 
 
 @pytest.mark.parametrize("M", [1, 20, 300])
