@@ -2,3 +2,5 @@
 # (E, M, N, K): more than 64 experts, 256 x 256 tiles
 MANY = [(70, 12000, 2100, 1152), (72, 14896, 2302, 1176), (70, 6000, 4096, 144), (130, 20000, 1100, 520),
         (300, 30000, 1030, 272)]
+# (tile, K): sums of more than 128 blocks, in the least sizes that take the tile
+LONG = [(tile, K) for K in (16400, 24592, 33000) for tile in range(10)] + [(0, 131071), (1, 131071), (4, 131071)]

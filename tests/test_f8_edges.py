@@ -1,6 +1,6 @@
 """The sizes of the GPU tests of the products' tiles do run what they are meant to (no GPU needed)."""
 import f8_tiles
-from f8_edges import MANY
+from f8_edges import LONG, MANY
 from test_f8_tile_choice import EDGES
 
 
@@ -14,3 +14,9 @@ def test_every_tile_has_a_size_in_the_tests():
 def test_many_experts_in_large_tiles():
     assert {f8_tiles.tiles()[t][:2] for t in f8_tiles.choices(MANY)} == {(256, 256)}
     assert all(E > 64 for E, *_ in MANY) and any(E > 128 for E, *_ in MANY)
+
+
+def test_long_sums_in_every_tile():
+    assert all(K > 128 * 128 for _, K in LONG) and {tile for tile, _ in LONG} == set(range(10))
+    for tile, K in LONG:
+        assert tile in f8_tiles.smallest(K, 0) and tile in f8_tiles.smallest(K, 8), (tile, K)

@@ -2,7 +2,8 @@
 import pytest
 import torch
 
-from f8_edges import MANY
+import f8_tiles
+from f8_edges import LONG, MANY
 from test_f8_gpu import (F8, blocks, check_product, codes, qr, reference, rows_in, say, scales_like,  # noqa: F401
                          sizes_of_groups)
 
@@ -34,6 +35,44 @@ def test_large_tiles_of_many_experts(qr, E, M, N, K, kind):  # noqa: F811
     lo, hi = int(offsets[0]), int(offsets[-1])
     assert bool((c[:lo] == 9.0).all()) and bool((c[hi:] == 9.0).all())
     check_groups(c, a, sa, rows, b, sb, offsets, (E, M, N, K))
+
+
+def uneven(rows, K, g):
+    """block scales over six powers of two, so that another block's would be far off"""
+    s = scales_like(rows, K, g)
+    return s.copy_(0.005 * torch.exp2(6 * torch.rand(s.shape, generator=g, device="cuda") - 3))
+
+
+@pytest.mark.parametrize("tile,K", LONG)
+def test_long_sums(qr, tile, K):  # noqa: F811
+    """more than 128 blocks: every buffer of the scales is filled again and read again"""
+    M, N = f8_tiles.smallest(K, 0)[tile]
+    say("long", tile, M, N, K)
+    g = torch.Generator(device="cuda").manual_seed(M + N + K)
+    a, sa = codes(M, K, g), uneven(M, K, g)
+    b, sb = codes(N, K, g), uneven(blocks(N), K, g)
+    _, c = rows_in(M, N, N + 1, torch.float16, 9.0)
+    qr.qr_gemm_f8(a, sa, b, sb, c)
+    check_product(c, *reference(a, sa, b, sb, None), (tile, M, N, K))
+    # the test can fail: with the scales that a buffer held before (16 blocks back the tokens', 128 the weights') most
+    # outputs would be out of tolerance (the weights' where more than the 16 codes of K = 16400 are that far on)
+    stale = [(sa.roll(16, 1), sb), (sa, torch.cat([sb[:, :128], sb[:, :-128]], 1))]
+    for x, y in stale[:2 if blocks(K) >= 192 else 1]:
+        want, tol = reference(a, x, b, y, None)
+        assert bool(((c.double() - want).abs() > tol + 2.0 ** -11 * (want.abs() + tol) + 2.0 ** -25).float().mean() > 0.5)
+    if K > 40000:
+        return
+    E = 8
+    M, N = f8_tiles.smallest(K, E)[tile]
+    say("long, grouped", tile, M, N, K)
+    tokens = max(1, M // 2)
+    a, sa = codes(tokens, K, g), uneven(tokens, K, g)
+    b, sb = codes(E * N, K, g).unflatten(0, (E, N)), uneven(E * blocks(N), K, g).unflatten(0, (E, blocks(N)))
+    offsets = sizes_of_groups("random", E, M, g)
+    rows = torch.randint(0, tokens, (M,), generator=g, device="cuda").to(torch.int32)
+    _, c = rows_in(M, N, N + 1, torch.float16, 9.0)
+    qr.qr_gemm_f8_grouped(a, sa, b, sb, offsets, c, rows=rows)
+    check_groups(c, a, sa, rows, b, sb, offsets, (tile, M, N, K))
 
 
 @pytest.mark.parametrize("M", [1, 20, 300])
