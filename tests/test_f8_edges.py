@@ -1,6 +1,6 @@
 """The sizes of the GPU tests of the products' tiles do run what they are meant to (no GPU needed)."""
 import f8_tiles
-from f8_edges import LONG, MANY
+from f8_edges import GRAPH_DENSE, GRAPH_GROUPED, LONG, MANY
 from test_f8_tile_choice import EDGES
 
 
@@ -20,3 +20,10 @@ def test_long_sums_in_every_tile():
     assert all(K > 128 * 128 for _, K in LONG) and {tile for tile, _ in LONG} == set(range(10))
     for tile, K in LONG:
         assert tile in f8_tiles.smallest(K, 0) and tile in f8_tiles.smallest(K, 8), (tile, K)
+
+
+def test_captured_products_take_large_tiles():
+    taken = [f8_tiles.tiles()[t] for t in f8_tiles.choices([(0, *s) for s in GRAPH_DENSE]
+                                                           + [(E, T * k, N, K) for T, k, E, N, K in GRAPH_GROUPED])]
+    assert all(waves != 0 for *_, waves in taken)    # k_tile_f8
+    assert (256, 256) in {t[:2] for t in taken[:3]} and (256, 256) in {t[:2] for t in taken[3:]}

@@ -3,8 +3,8 @@ import pytest
 import torch
 
 import f8_tiles
-from f8_edges import LONG, MANY
-from test_f8_gpu import (F8, blocks, check_product, codes, qr, reference, rows_in, say, scales_like,  # noqa: F401
+from f8_edges import GRAPH_DENSE, GRAPH_GROUPED, LONG, MANY
+from test_f8_gpu import (F8, NAN, blocks, check_product, codes, qr, reference, rows_in, say, scales_like,  # noqa: F401
                          sizes_of_groups)
 
 pytestmark = pytest.mark.gpu
@@ -96,3 +96,97 @@ def test_what_an_outlier_costs_its_group(qr, M, large, other, scale, bound):  # 
     assert bool((c == kept * scale).all()) and kept * scale == 1024
     lost = 1 - kept / all_of_it
     assert 0.85 * bound < lost < bound
+
+
+@pytest.mark.parametrize("M,N,K", GRAPH_DENSE)
+def test_captured_product(qr, M, N, K):  # noqa: F811
+    """a product in a graph takes what its inputs hold at each replay; on another stream than theirs too"""
+    say("captured", M, N, K)
+    g = torch.Generator(device="cuda").manual_seed(M + N + K)
+
+    def inputs():
+        return [codes(M, K, g), scales_like(M, K, g), codes(N, K, g), scales_like(blocks(N), K, g),
+                torch.randn(N, generator=g, device="cuda").half()]
+
+    held = inputs()
+    c, eager = torch.empty(M, N, dtype=torch.float16, device="cuda"), torch.empty(M, N, dtype=torch.float16, device="cuda")
+    qr.qr_gemm_f8(*held[:4], eager, bias=held[4])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qr.qr_gemm_f8(*held[:4], c, bias=held[4])
+    for i in range(4):
+        new = inputs()
+        for t, n in zip(held, new):
+            t.copy_(n)
+        c.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        check_product(c, *reference(*new), (M, N, K, i))
+        qr.qr_gemm_f8(*held[:4], eager, bias=held[4])         # eager work between the replays
+        assert torch.equal(c, eager)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    c.fill_(9.0)
+    torch.cuda.synchronize()
+    qr.qr_gemm_f8(*held[:4], c, bias=held[4], stream=side)
+    side.synchronize()
+    assert torch.equal(c, eager)
+
+
+@pytest.mark.parametrize("T,k,E,N,K", GRAPH_GROUPED)
+def test_captured_groups_follow_the_router(qr, T, k, E, N, K):  # noqa: F811
+    """the router, its experts' product over the tokens in place and the weighted sum in one graph: other logits give other
+    offsets and rows, the same graph the new product"""
+    say("captured groups", T, k, E, N, K)
+    g = torch.Generator(device="cuda").manual_seed(T + E + N + K)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    M = T * k
+    logits = torch.zeros(T, E, device="cuda")
+    weights, experts, offsets = torch.empty(T, k, device="cuda"), torch.empty(T, k, **i32), torch.empty(E + 1, **i32)
+    rows, place, ws = torch.empty(M, **i32), torch.empty(T, k, **i32), qr.alloc_route_workspace(T, E, k)
+    a, sa = codes(T, K, g), scales_like(T, K, g)
+    b, sb = codes(E * N, K, g).unflatten(0, (E, N)), scales_like(E * blocks(N), K, g).unflatten(0, (E, blocks(N)))
+    c, y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+
+    def run(stream=None):
+        qr.qr_route(logits, weights, experts, offsets, rows, place, renormalize=True, workspace=ws, stream=stream)
+        qr.qr_gemm_f8_grouped(a, sa, b, sb, offsets, c, rows=rows, stream=stream)
+        qr.qr_combine(c, place, weights, y, stream=stream)
+
+    def result():
+        torch.cuda.synchronize()
+        return [t.clone() for t in (weights, experts, offsets, rows, place, c, y)]
+
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    before = None
+    for i in range(4):
+        popular = torch.randn(E, generator=g, device="cuda") * i            # more and more unequal
+        logits.copy_(torch.randn(T, E, generator=g, device="cuda") + popular)
+        a.view(torch.uint8).copy_(codes(T, K, g).view(torch.uint8))
+        for t, fill in ((weights, NAN), (experts, 0), (offsets, 0), (rows, 0), (place, 0), (c, NAN), (y, NAN)):
+            t.fill_(fill)
+        graph.replay()
+        got = result()
+        run()                                                              # eager work between the replays
+        for x, want in zip(got, result()):
+            assert torch.equal(x, want)
+        assert int(offsets[0]) == 0 and int(offsets[-1]) == M
+        assert torch.equal(torch.bincount(experts.reshape(-1).long(), minlength=E), (offsets[1:] - offsets[:-1]).long())
+        assert before is None or not torch.equal(before, offsets)
+        before = offsets.clone()
+        check_groups(c, a, sa, rows, b, sb, offsets, (T, k, E, N, K, i))
+        exact = (weights.double()[:, :, None] * c.double()[place.long()]).sum(1)
+        size = (weights.double()[:, :, None] * c.double()[place.long()].abs()).sum(1)
+        tol = (k + 1) * 2.0 ** -24 * size
+        assert bool(((y.double() - exact).abs() <= tol + 2.0 ** -8 * (exact.abs() + tol) + 2.0 ** -134).all())
+    want = result()
+    c.fill_(NAN)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    run(side)
+    side.synchronize()
+    for x, w in zip(result(), want):
+        assert torch.equal(x, w)
