@@ -87,7 +87,8 @@ int qr_silu_mul_f8(qr_dtype dtype, const void* gu, size_t ldg, size_t M, size_t 
  *             128 x 128 block of b
  *   bias      N values of dtype, or NULL
  *   c         M x N, row stride ldc
- * K in 1..QR_MAX_ROW, N >= 1.  a, sa and b must be 16-byte aligned, lda and ldb
+ * K in 1..QR_MAX_ROW, N >= 1, ceil(M/256) * ceil(N/256) below 2^23 (tiles of a
+ * launch).  a, sa and b must be 16-byte aligned, lda and ldb
  * multiples of 16 below 2^23, ldsa a multiple of 4 up to 2^20: rows are read in
  * pieces of 16 bytes, so the bytes of a row of a, sa and b up to the next
  * multiple of 16 past its end must be readable (the last row's too); what they
@@ -113,8 +114,9 @@ int qr_gemm_f8(qr_dtype dtype, const uint8_t* a, size_t lda, const float* sa, si
  *             ones as equal; what such offsets make c is not defined, but
  *             nothing outside the arrays is touched
  *   c         M x N, row stride ldc
- * E in 1..QR_MAX_EXPERTS; (M / 256 + min(E, M)) * (N / 256) below 2^23, tiles of a
- * launch.  With rows, tokens * lda and 4 * tokens * ldsa must be below 2^32 - 2^18
+ * E in 1..QR_MAX_EXPERTS; (M/256 + min(E, M)) * ceil(N/256), the first quotient
+ * rounded down, below 2^23, tiles of a launch (QR_ERR_SIZE where they do not fit).
+ * With rows, tokens * lda and 4 * tokens * ldsa must be below 2^32 - 2^18
  * (rows are then addressed from a's start). */
 int qr_gemm_f8_grouped(qr_dtype dtype, const uint8_t* a, size_t lda, const float* sa, size_t ldsa,
                        const int32_t* rows, size_t tokens, const uint8_t* b, size_t ldb, size_t gb,
