@@ -23,9 +23,16 @@ namespace {
 // in the registers of a few lanes; weights are exponentials of differences to the
 // largest logit, so nothing overflows, summed in binary32.
 //
-// Bound by the chain of k reductions over a group's lanes, short calls by the launch.
-// Measured: 16 tokens over 32 experts, k = 4: 4.0 us; 16384 over 256, k = 8, bf16:
-// 18.7 us (k_choose 11, k_place 7.5), 4096 over 512: 18; the bytes alone would take 2.
+// Bound by the chain of k reductions over a group's lanes and, above 64 tokens, by
+// adding up the counts in k_place (its LDS atomics conflict in 74% of the cycles that
+// LDS is active in); short calls by the launch.
+// Measured, k = 8: 16384 tokens over 256 experts, bf16: 18.7 us (k_choose 11, k_place
+// 7.5), binary32: 23.6; 4096 over 512: 18 to 22 and 53; 4096 over 64: 9.4 and 11.5; 64
+// over 512: 17 and 45; the bytes alone would take 2 to 4 at most.  16 over 32, k = 4: 4.0.
+// Binary32 logits are read one by one and need a second reduction for the expert's
+// number; over 257 to 512 experts (more than 16 tokens) 16 lanes hold 32 each, which
+// passes the 128 registers that 1024 lanes have: 135 registers a lane are spilled, 147 up
+// to 64 tokens (16-bit logits: 3 up to 64 tokens, none above).
 // Placing the rows in a second launch costs about 2.5 us, but its workgroups need
 // all the counts, and no workgroup may wait for another.
 

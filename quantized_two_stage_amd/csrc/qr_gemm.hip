@@ -18,9 +18,9 @@
 // A stage of k_tile, ns, with 256 workgroups: 64x128 365, without its matrix
 // instructions 348, without its reads of LDS 373, without its loads 270;
 // 128x128 557, 471, 494, 431; 256x256 1661, 1376, 1748, 1105.
-// Measured (cold weights): 1 token over 8192x8192 weights 12 to 12.6 us, 5.3
+// Measured (cold weights): 1 token over 8192x8192 weights 11.9 to 12.6 us, 5.3
 // to 5.6 TB/s (plain reads reach 6.8); 48 tokens, 8192x4096: 11.1 to 13 us;
-// 8192^3: 424 to 442 us, 2490 to 2590 TOPS, the matrix units busy 67% of the
+// 8192^3: 420 to 442 us, 2490 to 2620 TOPS, the matrix units busy 67% of the
 // time (a library product of the same codes without scales: 528 us).
 #include <type_traits>
 #include <utility>

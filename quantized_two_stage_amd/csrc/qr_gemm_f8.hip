@@ -177,7 +177,8 @@ __device__ __forceinline__ size_t first_row(const F8Args& g, const Job& job) {
 // one block each.  Bound by the loads to LDS up to 128 x 128 (60 bytes/ns a CU), at
 // 256 x 256 by the matrix units, and by its ends where sums are short: a tile of 256
 // x 256 takes 1.67 us a block and 9 us besides (8192 x 8192: K = 512 63 us, K = 8192
-// 465 on the same card).
+// 465 on the same card).  128 x 256 spills 2 of its 256 registers, outside the stages;
+// no other tile spills any.
 //
 // The tokens' scales come 8 blocks at a time (two 16-byte pieces a row), one load
 // a lane, into the one of two buffers that is not in use.

@@ -17,10 +17,12 @@ namespace qr {
 // that (6000 a ns where they are read once, else 5300): of the shorter of the two
 // `once` or `again` percent are added.
 // Fitted to the times of all tiles at 380 sizes (1 to 8192 tokens, sums and
-// channels of 64 to 16384, one product or 4 to 128 experts, cold weights).  The
-// tile that choose_f8_tile takes against the fastest at each, and at 100 more of
-// small groups: 1.00 at the median; one product within 1.11 at nine of ten and 1.45 at
-// worst, groups within 1.12 and 1.35.
+// channels of 64 to 16384, one product or 4 to 128 experts, cold weights) and 100
+// more of small groups.  The tile that choose_f8_tile takes against the fastest at
+// each of these: 1.00 at the median; one product within 1.11 at nine of ten and 1.45
+// at worst (206 tokens, 9263 x 12902), groups within 1.12 and 1.35.  At 304 sizes
+// that the fit has not seen: one product 1.00, 1.13 and 1.45 (405 tokens, 2048 x
+// 16128), groups 1.01, 1.17 and 1.42 (88 rows over 4 experts of 1095 x 100).
 struct F8Tile {
   uint32_t bm, bn;                    // tokens and channels
   uint32_t wm, wn;                    // waves; wn == 0: wm waves that share the sum
@@ -59,7 +61,7 @@ constexpr uint32_t f8_tile_rows_likely(uint32_t bm, uint32_t M, uint32_t E) {
 
 // Whether most weights are read by one workgroup alone, and go past the caches:
 // one row of tiles, or experts of half a tile's rows on average.  Weights of 32
-// experts, 2048 x 8192, us: 64 rows in tiles of 8 69 (through the caches 77), of 16
+// experts, 2048 x 8192, us: 64 rows in tiles of 8 67 to 69 (through the caches 77), of 16
 // 82 (90); 2048 x 4096: 256 rows in tiles of 16 53 (57), 512 rows in tiles of 32 61
 // (64), but in tiles of 16 74 (67).
 constexpr bool f8_weights_once(uint32_t bm, uint32_t M, uint32_t E) {
@@ -94,8 +96,11 @@ constexpr bool f8_grid_fits(const F8Tile& t, uint32_t M, uint32_t N, uint32_t E)
 inline int choose_f8_tile(uint32_t M, uint32_t N, uint32_t K, uint32_t E) {
   if (E == 0 && M <= kF8Tiles[0].bm) return 0;
   // Few rows an expert, and mostly weights to read: the smallest tile that reads
-  // them once.  The estimate alone takes wider ones there: 64 rows over 32 experts of
-  // 2048 x 8192 take 67 us in tiles of 8 x 16, 95 in 64 x 128.
+  // them once (of those that are 8, 16 and 32 rows high and fastest there).  The estimate
+  // alone takes wider ones: 64 rows over 32 experts of 2048 x 8192 take 67 to 69 us in
+  // tiles of 8 x 16, 95 in 64 x 128.  At 135 of 460 timed sizes of groups the two differ:
+  // against the fastest tile this rule takes 1.00 at the median, 1.13 at nine of ten and
+  // 1.31 at worst, the estimate 1.08, 1.27 and 1.67.
   if (E != 0)
     for (int i : {0, 2, 3})
       if (f8_weights_once(kF8Tiles[i].bm, M, E)) {

@@ -175,9 +175,9 @@ hipError_t rows_twice(const Op& op, const RowsOut& o, hipStream_t st) {
 // 1024 x 1 56; one row of 8192 3.4, 3.4, 4.2, 5.9; 1024 rows of 5003 with 640
 // lanes 14.4, with 1024 lanes 19.9 (exact codes have added 0.3 to 3 us since).
 // Rows that are whole vectors apart from the others: the former with the
-// latter's loads take 113 instead of 98 (256 x 4).  The norm of lengths of 16385
-// to 32767 that are no multiple of 8 needs more than the 128 registers that 1024
-// lanes have, and 12 are spilled: 500 rows of 20003 take 28.6, of 20000 22.1.
+// latter's loads take 113 instead of 98 (256 x 4).  Lengths of 16385 to 32768 hold
+// four vectors a lane, in the 128 registers that 1024 lanes have: 500 rows of
+// 20000 take 22.7, of 20003 25.6, of 30000 29.9, of 30001 33.4.
 template <class Op, int E>
 hipError_t rows_by_length(const Op& op, const RowsOut& o, hipStream_t st) {
   if (o.d <= 512) return rows_in_registers<Op, true, 1, E>(op, o, st);
