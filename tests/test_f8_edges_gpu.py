@@ -3,9 +3,9 @@ import pytest
 import torch
 
 import f8_tiles
-from f8_edges import GRAPH_DENSE, GRAPH_GROUPED, LONG, MANY
-from test_f8_gpu import (F8, NAN, blocks, check_product, codes, qr, reference, rows_in, say, scales_like,  # noqa: F401
-                         sizes_of_groups)
+from f8_edges import GRAPH_DENSE, GRAPH_GROUPED, LONG, MANY, ROUTES
+from test_f8_gpu import (F8, INF, NAN, TYPES, blocks, check_product, check_route, codes, qr, reference, route,  # noqa: F401
+                         rows_in, say, scales_like, sizes_of_groups)
 
 pytestmark = pytest.mark.gpu
 
@@ -190,3 +190,19 @@ def test_captured_groups_follow_the_router(qr, T, k, E, N, K):  # noqa: F811
     side.synchronize()
     for x, w in zip(result(), want):
         assert torch.equal(x, w)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("T,E,k", ROUTES)
+def test_route_in_every_kernel(qr, T, E, k, dtype):  # noqa: F811
+    """values that lie close together, so that 16-bit ones are often equal, and some that are not numbers"""
+    g = torch.Generator(device="cuda").manual_seed(T + E + k)
+    for renormalize in (False, True):
+        say("route", T, E, k, dtype, renormalize)
+        logits = torch.randn(T, E + 5, generator=g, device="cuda").to(TYPES[dtype])[:, 2:E + 2]
+        if T > 4:
+            logits[0] = -INF
+            logits[1, E - 1], logits[2, 0] = NAN, INF
+            logits[3, ::2] = -INF
+            logits[4] = 0.0
+        check_route(logits, k, renormalize, route(qr, logits, k, renormalize), (T, E, k, dtype, renormalize))

@@ -2,6 +2,7 @@
 import re
 
 import f8_tiles
+from f8_edges import ROUTES, kernel_of_route
 
 from quantized_two_stage_amd import qr
 
@@ -22,12 +23,9 @@ def test_router():
     for dtype in (*TYPES, 3):
         for E in EXPERTS:
             for T in TOKENS:
-                # lanes to a token and logits to a lane
-                G, V = ((8, 8) if E <= 64 else (16, 8) if E <= 128 else (16, 16) if E <= 256 else (64, 16) if E > 512 else
-                        (64, 8) if T <= 16 else (16, 32))
-                lanes = 256 if T <= 64 and E <= 256 and T * G <= 256 else 1024
-                reached.add((dtype, G, V, lanes, int(T <= 64)))
+                reached.add((dtype, *kernel_of_route(T, E)))
     assert held("k_choose", *"iiiib") == reached
+    assert {x[1:] for x in reached} == {kernel_of_route(T, E) for T, E, _ in ROUTES}       # each has a test
 
 
 def test_products():
